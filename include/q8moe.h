@@ -592,6 +592,117 @@ int moe_r8_ffn_batched_noalloc(const moe_r8_ffn_desc *descs, int64_t n_desc, int
                                void *stream);
 
 /* ---------------------------------------------------------------------------
+ * 8-bit integer products with one scale per token and one per output channel.
+ * The codes of a row share one fp32 scale, so an output is one exact int32 sum
+ * over all of k and one rescale at the end (a Q8_0 product rescales every
+ * block of 32).
+ *
+ * Row rule: scale s = max|x| / 127 (IEEE fp32 division); code = x / s rounded
+ * to nearest, ties away from zero, decided on the exact quotient, saturating
+ * at +-127 (reachable beyond max|x| only where s is an fp32 subnormal); s = 0
+ * (a zero row, or one whose s underflows) gives zero codes.  A row that holds
+ * a NaN or an infinity gets s = NaN and zero codes, so that what is computed
+ * from it is NaN.
+ *
+ * Types of activations and outputs: */
+typedef enum q8_type {
+    Q8_T_F32 = 0,
+    Q8_T_F16 = 1,    /* IEEE binary16 */
+    Q8_T_BF16 = 2,
+    Q8_T_I8 = 3      /* codes with a scale per row (activations only) */
+} q8_type;
+
+/* i8_quantize_rows -- rows of x (fp32, binary16 or bfloat16) to codes and
+ * scales; used for tokens at every call and for a weight matrix [n][k] once at
+ * load (its rows are the output channels).
+ *   x      [n_rows][x_row_stride], 16-byte aligned, x_row_stride in elements,
+ *          >= k when n_rows > 1, a multiple of 16 bytes
+ *   q      int8 [n_rows][q_row_stride], 16-byte aligned, q_row_stride >= k
+ *          when n_rows > 1, a multiple of 16 (bytes past k are not written)
+ *   scale  fp32 [n_rows]
+ * n_rows >= 0, 0 < k <= 131040, k % 32 == 0 (larger k: Q8_E_UNSUPPORTED, the
+ * int32 sums of the products below could overflow); strides at most 4 MiB per
+ * row (Q8_E_UNSUPPORTED); x and q must not overlap.
+ */
+int i8_quantize_rows(const void *x, int x_type, int64_t x_row_stride, int8_t *q,
+                     int64_t q_row_stride, float *scale, int64_t n_rows, int64_t k, void *stream);
+
+/* i8_matmul -- y[t][j] = (sum_i cx[t][i] * cw[j][i]) * sx[t] * sw[j] + bias[j]
+ * for m token rows: the int32 sum is exact, the scales and the bias are applied
+ * in fp32 in that order, and the result is rounded once to y's type (values
+ * beyond binary16's range become infinities).
+ *   x        x_type Q8_T_I8: codes [m][x_row_stride] and x_scale fp32 [m];
+ *            else rows of that type, quantized by the row rule inside the call
+ *            (the results are bitwise those of i8_quantize_rows followed by
+ *            this call on codes), x_scale ignored.  16-byte aligned, the row
+ *            stride (elements) a multiple of 16 bytes, >= k when m > 1
+ *   w        int8 [n][w_row_stride], 16-byte aligned, w_row_stride a multiple
+ *            of 16, >= k when n > 1;  w_scale fp32 [n]
+ *   bias     fp32 [n], or NULL
+ *   y        y_type (Q8_T_F32, Q8_T_F16, Q8_T_BF16) [m][y_row_stride],
+ *            y_row_stride >= n when m > 1 (elements past n are not written)
+ *   ws       i8_workspace_bytes(m, k) bytes, 256-byte aligned, where x is not
+ *            codes (else ignored); contents need not be initialised; not shared
+ *            by calls that may run concurrently
+ * m, n >= 0, 0 < k <= 131040, k % 32 == 0; codes may be any int8 value, -128
+ * included; row strides at most 4 MiB, m and n at most 2^27 (Q8_E_UNSUPPORTED).
+ * An output does not depend on how many rows a call has (bitwise): the sum is
+ * exact and the rest is per element.
+ *
+ * i8_up_gate_swiglu -- the gated product: with the combined weight w
+ * [2*n_ff][k] (gate rows first, the layout of q8_0_up_gate_swiglu_batched) and
+ * w_scale [2*n_ff],  h[t][j] = silu(g) * u = g / (1 + exp(-g)) * u  in fp32,
+ * g and u the i8_matmul values (without bias) of rows j and n_ff + j, rounded
+ * once to h's type.  Everything else as i8_matmul.
+ */
+size_t i8_workspace_bytes(int64_t m, int64_t k);
+
+int i8_matmul(const void *x, int x_type, int64_t x_row_stride, const float *x_scale,
+              const int8_t *w, int64_t w_row_stride, const float *w_scale, const float *bias,
+              void *y, int y_type, int64_t y_row_stride, int64_t n, int64_t k, int64_t m,
+              void *ws, size_t ws_bytes, void *stream);
+
+int i8_up_gate_swiglu(const void *x, int x_type, int64_t x_row_stride, const float *x_scale,
+                      const int8_t *w, int64_t w_row_stride, const float *w_scale, void *h,
+                      int h_type, int64_t h_row_stride, int64_t n_ff, int64_t k, int64_t m,
+                      void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * logprob_rows -- log probabilities over rows of logits, as the vocabulary
+ * products of this library write them (fp32), or in binary16 or bfloat16:
+ *   M = max_j x[t][j],  S = sum_j exp(x[t][j] - M),  lse[t] = M + log S
+ *   logprob[t][i] = x[t][tokens[t][i]] - lse[t]
+ *   entropy[t] = log S - (sum_j exp(x[t][j] - M) * (x[t][j] - M)) / S
+ *   top_ids[t][0..n_top), top_logprobs[t][0..n_top): the n_top largest logits
+ *   in descending order, ties to the lowest index, and their log probabilities
+ * Everything is computed in fp32, sums of lanes and of parts of a row in trees
+ * of fixed shape (results are the same bits at every call).
+ *   logits   [m][row_stride] of `type`, aligned to its element; row_stride in
+ *            elements, >= n_vocab when m > 1 (any value: rows need no padding)
+ *   tokens   int32 [m][n_given]; a token outside [0, n_vocab) gives NaN
+ *   logprob  fp32 [m][n_given]; lse, entropy  fp32 [m], each may be NULL
+ *   top_ids  int32 [m][n_top], top_logprobs  fp32 [m][n_top]
+ * A logit of -infinity is a token of probability zero: log probability
+ * -infinity, last in the order (the lowest index first).  A row of nothing
+ * else: lse and every log probability -infinity, entropy 0.  A row with a NaN
+ * or +infinity: lse, entropy and every log probability NaN; top_ids are
+ * distinct indices of the row, with +infinity first and NaN last.
+ * m >= 0, n_vocab > 0, n_given >= 0, 0 <= n_top <= n_vocab (Q8_E_SHAPE);
+ * n_top <= 64, n_given <= 1024, n_vocab <= 2^30, m <= 2^24 (Q8_E_UNSUPPORTED).
+ * tokens and logprob may be NULL when n_given is 0, the top arrays when n_top
+ * is 0.  Outputs must not overlap the inputs.
+ * Workspace: logprob_workspace_bytes(m, n_vocab, n_top) bytes (0 for sizes the
+ * call refuses), 256-byte aligned; contents need not be initialised; not
+ * shared by calls that may run concurrently.
+ */
+size_t logprob_workspace_bytes(int64_t m, int64_t n_vocab, int64_t n_top);
+
+int logprob_rows(const void *logits, int type, int64_t row_stride, const int32_t *tokens,
+                 int64_t n_given, float *logprob, float *lse, float *entropy, int32_t *top_ids,
+                 float *top_logprobs, int64_t m, int64_t n_vocab, int64_t n_top, void *ws,
+                 size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Validation exports, for testing: the kernels of the product path, built
  * with an extra output (a compile-time flag, so the product path itself is
  * unchanged), that write the exact int32 block sums s = sum_j qw[j]*qx[j] of

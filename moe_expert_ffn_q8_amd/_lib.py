@@ -10,6 +10,7 @@ this module raises.
 """
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -143,6 +144,15 @@ _SIGS = {
     "moe_r8_ffn_fused": (_int, [ctypes.POINTER(MoeR8FfnDesc), _i64, _i64, _i64, _i64, _vp]),
     "kq_matvec_batched": (_int, [_int, ctypes.POINTER(KqMatvecDesc), _i64, _vp]),
     "q4_k_matvec": (_int, [_vp, _vp, _vp, _i64, _i64, _vp]),
+    "i8_quantize_rows": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _i64, _vp]),
+    "i8_workspace_bytes": (_size, [_i64, _i64]),
+    "i8_matmul": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _int, _i64, _i64, _i64,
+                         _i64, _vp, _size, _vp]),
+    "i8_up_gate_swiglu": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _int, _i64, _i64,
+                                 _i64, _i64, _vp, _size, _vp]),
+    "logprob_workspace_bytes": (_size, [_i64, _i64, _i64]),
+    "logprob_rows": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                            _vp, _size, _vp]),
     "q5_k_matvec": (_int, [_vp, _vp, _vp, _i64, _i64, _vp]),
 }
 
@@ -913,6 +923,211 @@ def moe_r8_ffn_fused(layer, n_embd, n_ff, n_expert):
 def moe_error_word(ws):
     """The int32 error word at the start of a MoE workspace (1 = an id was out of range)."""
     return int(ws[:4].view(torch.int32).item())
+
+
+# ---------------------------------------------------------------------------
+# 8-bit products with one scale per token and per output channel, and log
+# probabilities of logit rows.
+
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
+
+
+def _rows(t, name, dtypes):
+    """(type, row stride) of a 2-D GPU tensor whose rows are contiguous."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}, expected one of {[str(d) for d in dtypes]}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a GPU tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return _TYPES[t.dtype], t.stride(0)
+
+
+def _vector(t, n, dtype, name):
+    if t is None:
+        return
+    _need(t, dtype, name)
+    if t.numel() != n:
+        raise ValueError(f"{name}: {t.numel()} elements, expected {n}")
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+
+
+def _on_device(t, fn, *args):
+    """fn(*args, stream) on t's device (made current for the call if it is
+    not) and its current stream."""
+    if t.device.index == torch.cuda.current_device():
+        return fn(*args, _stream(t))
+    with torch.cuda.device(t.device):
+        return fn(*args, _stream(t))
+
+
+_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+_ACTS = _FLOATS + (torch.int8,)
+_INT8 = (torch.int8,)
+
+
+def i8_quantize_rows(x, q=None, scale=None):
+    """x: fp32, fp16 or bf16 [n_rows][k] (or [k]) -> (q int8 [n_rows][k],
+    scale fp32 [n_rows]): codes by row with scale = max|x| / 127.  Rows may
+    have a stride.  For a weight matrix [n][k], once at load, and for tokens
+    whose codes serve several products."""
+    if x.dim() == 1:
+        x = x.unsqueeze(0)
+    xt, xs = _rows(x, "x", _FLOATS)
+    n_rows, k = x.shape
+    if q is None:
+        q = torch.empty((n_rows, k), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(n_rows, dtype=torch.float32, device=x.device)
+    _, qs = _rows(q, "q", _INT8)
+    _shape(q, (n_rows, k), "q")
+    _vector(scale, n_rows, torch.float32, "scale")
+    _one_device(x, q, scale)
+    _check("i8_quantize_rows", _on_device(x, _lib.i8_quantize_rows, _ptr(x), xt, xs, _ptr(q), qs,
+                                          _ptr(scale), n_rows, k))
+    return q, scale
+
+
+def i8_workspace_bytes(m, k):
+    return int(_lib.i8_workspace_bytes(m, k))
+
+
+def i8_workspace(m, k, device):
+    """Workspace of a product whose m activation rows are not codes."""
+    n = i8_workspace_bytes(m, k)
+    if n == 0:
+        raise Q8Error("i8_workspace_bytes", -4)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _i8_operands(x, w, w_scale, x_scale, ws):
+    xt, xs = _rows(x, "x", _ACTS)
+    _, wst = _rows(w, "w", _INT8)
+    m, k = x.shape
+    if w.shape[1] != k:
+        raise ValueError(f"w: rows of {w.shape[1]} codes, x has {k}")
+    _vector(w_scale, w.shape[0], torch.float32, "w_scale")
+    if xt == 3:
+        if x_scale is None:
+            raise ValueError("x_scale: needed with int8 codes")
+        _vector(x_scale, m, torch.float32, "x_scale")
+        ws = None
+    else:
+        if x_scale is not None:
+            raise ValueError("x_scale: given with rows that are not int8 codes")
+        _need(ws, torch.uint8, "ws")
+    _one_device(x, w, w_scale, x_scale, ws)
+    return xt, xs, wst, m, k, ws
+
+
+def i8_matmul(x, w, w_scale, x_scale=None, bias=None, y=None, dtype=torch.float32, ws=None):
+    """y[t][j] = (sum_i x[t][i] w[j][i]) * x_scale[t] * w_scale[j] (+ bias[j]).
+    x: int8 codes [m][k] with x_scale, or fp32 / fp16 / bf16 rows, quantized
+    inside (ws: i8_workspace(m, k)); w: int8 [n][k]; w_scale, bias: fp32 [n].
+    y: fp32, fp16 or bf16 [m][n] (made with `dtype` if not given)."""
+    xt, xs, wst, m, k, ws = _i8_operands(x, w, w_scale, x_scale, ws)
+    n = w.shape[0]
+    if y is None:
+        y = torch.empty((m, n), dtype=dtype, device=x.device)
+    yt, ys = _rows(y, "y", _FLOATS)
+    _shape(y, (m, n), "y")
+    _vector(bias, n, torch.float32, "bias")
+    _one_device(x, y, bias)
+    _check("i8_matmul", _on_device(
+        x, _lib.i8_matmul, _ptr(x), xt, xs, _ptr(x_scale), _ptr(w), wst, _ptr(w_scale), _ptr(bias),
+        _ptr(y), yt, ys, n, k, m, _ptr(ws), 0 if ws is None else ws.numel()))
+    return y
+
+
+def i8_up_gate_swiglu(x, w, w_scale, x_scale=None, h=None, dtype=torch.float32, ws=None):
+    """h[t][j] = silu(g) * u with g, u the products of rows j and n_ff + j of
+    the combined weight w int8 [2*n_ff][k] (gate rows first); x, x_scale, ws
+    as for i8_matmul; h: fp32, fp16 or bf16 [m][n_ff]."""
+    xt, xs, wst, m, k, ws = _i8_operands(x, w, w_scale, x_scale, ws)
+    if w.shape[0] % 2:
+        raise ValueError(f"w: {w.shape[0]} rows, expected gate and up rows of one number")
+    n_ff = w.shape[0] // 2
+    if h is None:
+        h = torch.empty((m, n_ff), dtype=dtype, device=x.device)
+    ht, hs = _rows(h, "h", _FLOATS)
+    _shape(h, (m, n_ff), "h")
+    _one_device(x, h)
+    _check("i8_up_gate_swiglu", _on_device(
+        x, _lib.i8_up_gate_swiglu, _ptr(x), xt, xs, _ptr(x_scale), _ptr(w), wst, _ptr(w_scale),
+        _ptr(h), ht, hs, n_ff, k, m, _ptr(ws), 0 if ws is None else ws.numel()))
+    return h
+
+
+class LogprobOut(NamedTuple):
+    """Outputs of logprob_rows; top_ids and top_logprobs are None without
+    alternatives, logprob without given tokens."""
+    logprob: Optional[torch.Tensor]        # fp32 [m][n_given]
+    lse: torch.Tensor                      # fp32 [m]
+    entropy: torch.Tensor                  # fp32 [m]
+    top_ids: Optional[torch.Tensor]        # int32 [m][n_top]
+    top_logprobs: Optional[torch.Tensor]   # fp32 [m][n_top]
+
+
+def logprob_outputs(m, n_given, n_top, device):
+    """Output tensors for logprob_rows (its `out`)."""
+    def new(*shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device=device)
+    return LogprobOut(new(m, n_given) if n_given else None, new(m), new(m),
+                      new(m, n_top, dtype=torch.int32) if n_top else None,
+                      new(m, n_top) if n_top else None)
+
+
+def logprob_workspace_bytes(m, n_vocab, n_top):
+    return int(_lib.logprob_workspace_bytes(m, n_vocab, n_top))
+
+
+def logprob_workspace(m, n_vocab, n_top, device):
+    n = logprob_workspace_bytes(m, n_vocab, n_top)
+    if n == 0:
+        raise Q8Error("logprob_workspace_bytes", -4)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def logprob_rows(logits, tokens=None, n_top=0, ws=None, out=None):
+    """Log probabilities of the given tokens (int32 [m] or [m][n_given]), log
+    sum exp, entropy and the n_top largest logits (ties to the lowest index)
+    of each row of logits, fp32 / fp16 / bf16 [m][n_vocab].  ws:
+    logprob_workspace(m, n_vocab, n_top).  Returns a LogprobOut (`out` if
+    given)."""
+    t, stride = _rows(logits, "logits", _FLOATS)
+    m, n_vocab = logits.shape
+    if n_top < 0:
+        raise Q8Error("logprob_rows", -2)
+    n_given = 0
+    if tokens is not None:
+        _need(tokens, torch.int32, "tokens")
+        n_given = 1 if tokens.dim() == 1 else tokens.shape[-1]
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != m:
+            raise ValueError(f"tokens: shape {tuple(tokens.shape)}, expected [{m}] or [{m}][n_given]")
+    if out is None:
+        out = logprob_outputs(m, n_given, n_top, logits.device)
+    logprob = out.logprob if n_given else None
+    ids, top = (out.top_ids, out.top_logprobs) if n_top else (None, None)
+    if (n_given and logprob is None) or (n_top and (ids is None or top is None)):
+        raise ValueError("out: lacks an output that this call has")
+    _vector(logprob, m * n_given, torch.float32, "logprob")
+    _vector(out.lse, m, torch.float32, "lse")
+    _vector(out.entropy, m, torch.float32, "entropy")
+    _vector(ids, m * n_top, torch.int32, "top_ids")
+    _vector(top, m * n_top, torch.float32, "top_logprobs")
+    _need(ws, torch.uint8, "ws")
+    _one_device(logits, tokens, ws, *out)
+    _check("logprob_rows", _on_device(
+        logits, _lib.logprob_rows, _ptr(logits), t, stride, _ptr(tokens), n_given, _ptr(logprob),
+        _ptr(out.lse), _ptr(out.entropy), _ptr(ids), _ptr(top), m, n_vocab, n_top, _ptr(ws),
+        0 if ws is None else ws.numel()))
+    return out
 
 
 # Raw access for tests of the argument checks (no tensors needed).
