@@ -20,7 +20,7 @@ ARCH = "gfx950"
 
 SOURCES = ["quantize.hip", "stream.hip", "step.hip", "ffn.hip", "small_m.hip", "moe.hip",
            "moe_gemm.hip", "moe_r8.hip", "gemm.hip", "r8.hip", "r8_mm.hip", "kquant.hip", "probe.hip",
-           "i8_quantize.hip", "i8_gemm.hip", "logprob.hip", "abi.cpp", "abi_i8.cpp"]
+           "i8_quantize.hip", "i8_gemm.hip", "i8_stream.hip", "logprob.hip", "abi.cpp", "abi_i8.cpp"]
 
 # no packed fp32 instructions in device code; MFMA results in VGPRs (the
 # rescale of each int32 block tile then needs no accumulator-register copies)

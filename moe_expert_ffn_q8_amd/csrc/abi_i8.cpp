@@ -60,19 +60,23 @@ int i8_product(const void *x, int x_type, int64_t x_row_stride, const float *x_s
     a.w = w; a.w_scale = w_scale; a.bias = bias; a.y = y;
     a.w_stride = w_row_stride; a.y_stride = y_row_stride;
     a.n = n; a.k = k; a.m = m; a.y_type = y_type;
-    if (codes) {
-        a.x = (const int8_t *)x; a.x_scale = x_scale; a.x_stride = x_row_stride;
-    } else {
+    if (!codes && (!ws || ws_bytes < i8_workspace_bytes(m, k))) return Q8_E_WORKSPACE;
+    if (!codes && !aligned(ws, 256)) return Q8_E_ALIGN;
+    a.x = (const int8_t *)x; a.x_scale = x_scale; a.x_stride = x_row_stride;
+    if (q8::i8_inline_ok(m, k))
+        return hip_status(q8::launch_i8_stream(a, x, x_type, x_row_stride * type_bytes(x_type),
+                                               gated, st));
+    if (!codes) {
         // workspace: m rows of codes, then m scales
-        if (!ws || ws_bytes < i8_workspace_bytes(m, k)) return Q8_E_WORKSPACE;
-        if (!aligned(ws, 256)) return Q8_E_ALIGN;
         int8_t *q = (int8_t *)ws;
         float *s = (float *)(q + m * up16(k));
         if (int rc = q8::launch_i8_quantize(x, x_type, x_row_stride, q, up16(k), s, m, k, st))
             return hip_status(rc);
         a.x = q; a.x_scale = s; a.x_stride = up16(k);
     }
-    return hip_status(q8::launch_i8_product(a, gated, st));
+    return hip_status(m <= q8::kI8StreamMaxM
+                          ? q8::launch_i8_stream(a, nullptr, Q8_T_I8, 0, gated, st)
+                          : q8::launch_i8_gemm(a, gated, st));
 }
 
 }  // namespace

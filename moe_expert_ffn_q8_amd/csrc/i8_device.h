@@ -111,11 +111,23 @@ __device__ __forceinline__ float silu_mul(float g, float u)
     return g * __builtin_amdgcn_rcpf(d) * u;
 }
 
-// One value, rounded to nearest even to the output's type.
+// One value, rounded to nearest even to the output's type.  (The value is
+// pinned as fp32 first: a last product merged with the conversion, as
+// v_fma_mixlo_f16 does, would round once where another kernel rounds twice.)
 template <int T>
 __device__ __forceinline__ void store_out(void *y, int64_t i, float v)
 {
+    if constexpr (T == Q8_T_F16) asm("" : "+v"(v));
     ((typename Elem<T>::type *)y)[i] = (typename Elem<T>::type)v;
+}
+
+// Up to 4 consecutive values.
+template <int T>
+__device__ __forceinline__ void store_run(void *y, int64_t i, const float (&v)[4], int left)
+{
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (r < left) store_out<T>(y, i + r, v[r]);
 }
 
 }  // namespace q8

@@ -228,7 +228,7 @@ int launch_type(const I8Args &a, bool gated, hipStream_t stream)
 
 }  // namespace
 
-int launch_i8_product(const I8Args &a, bool gated, hipStream_t stream)
+int launch_i8_gemm(const I8Args &a, bool gated, hipStream_t stream)
 {
     if (a.y_type == Q8_T_F32) return launch_type<Q8_T_F32>(a, gated, stream);
     if (a.y_type == Q8_T_F16) return launch_type<Q8_T_F16>(a, gated, stream);

@@ -31,7 +31,16 @@ struct I8Args {
 int launch_i8_quantize(const void *x, int type, int64_t x_stride, int8_t *q, int64_t q_stride,
                        float *scale, int64_t n_rows, int64_t k, hipStream_t stream);
 
-int launch_i8_product(const I8Args &a, bool gated, hipStream_t stream);
+// Few token rows (m <= kI8StreamMaxM), weights streamed once.  With xf the
+// token rows are taken as given (xf_type, Q8_T_I8 included; bytes per row
+// xf_stride) where i8_inline_ok, and a.x is not read.
+constexpr int64_t kI8StreamMaxM = 64;
+bool i8_inline_ok(int64_t m, int64_t k);
+int launch_i8_stream(const I8Args &a, const void *xf, int xf_type, int64_t xf_stride, bool gated,
+                     hipStream_t stream);
+
+// Many token rows, on tiles of both operands.
+int launch_i8_gemm(const I8Args &a, bool gated, hipStream_t stream);
 
 // Log probabilities, already validated.
 struct LogprobArgs {
