@@ -929,47 +929,55 @@ def moe_error_word(ws):
 # 8-bit products with one scale per token and per output channel, and log
 # probabilities of logit rows.
 
-_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
+_FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_INT8 = {torch.int8: 3}
+_ACTS = {**_FLOATS, **_INT8}
 
 
-def _rows(t, name, dtypes):
-    """(type, row stride) of a 2-D GPU tensor whose rows are contiguous."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: {t.dtype}, expected one of {[str(d) for d in dtypes]}")
+def _rows(t, name, types):
+    """(type, row stride, rows, columns) of a 2-D GPU tensor whose rows are
+    contiguous."""
+    code = types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: {t.dtype}, expected one of {[str(d) for d in types]}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a GPU tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(shape)}")
+    stride = t.stride()
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return _TYPES[t.dtype], t.stride(0)
+    return code, stride[0], shape[0], shape[1]
 
 
 def _vector(t, n, dtype, name):
-    if t is None:
-        return
     _need(t, dtype, name)
     if t.numel() != n:
         raise ValueError(f"{name}: {t.numel()} elements, expected {n}")
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+def _on(device, *ts):
+    """Every tensor of a call on `device`."""
+    for t in ts:
+        if t is not None and t.device != device:
+            _one_device(*ts)
+            raise ValueError(f"tensors on several devices: {device}, {t.device}")
 
 
-def _on_device(t, fn, *args):
-    """fn(*args, stream) on t's device (made current for the call if it is
-    not) and its current stream."""
-    if t.device.index == torch.cuda.current_device():
-        return fn(*args, _stream(t))
-    with torch.cuda.device(t.device):
-        return fn(*args, _stream(t))
-
-
-_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
-_ACTS = _FLOATS + (torch.int8,)
-_INT8 = (torch.int8,)
+def _enqueue(name, fn, device, *args):
+    """fn(*args, stream) on the device (made current for the call if it is not)
+    and its current stream.  (torch.cuda.current_stream() builds a Stream object
+    at 2 us a call; the raw handle is read in 0.1.)"""
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise Q8Error(name, rc)
 
 
 def i8_quantize_rows(x, q=None, scale=None):
@@ -979,18 +987,19 @@ def i8_quantize_rows(x, q=None, scale=None):
     whose codes serve several products."""
     if x.dim() == 1:
         x = x.unsqueeze(0)
-    xt, xs = _rows(x, "x", _FLOATS)
-    n_rows, k = x.shape
+    xt, xs, n_rows, k = _rows(x, "x", _FLOATS)
     if q is None:
         q = torch.empty((n_rows, k), dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty(n_rows, dtype=torch.float32, device=x.device)
-    _, qs = _rows(q, "q", _INT8)
-    _shape(q, (n_rows, k), "q")
+    _, qs, q_rows, q_k = _rows(q, "q", _INT8)
+    if (q_rows, q_k) != (n_rows, k):
+        raise ValueError(f"q: shape {(q_rows, q_k)}, expected {(n_rows, k)}")
     _vector(scale, n_rows, torch.float32, "scale")
-    _one_device(x, q, scale)
-    _check("i8_quantize_rows", _on_device(x, _lib.i8_quantize_rows, _ptr(x), xt, xs, _ptr(q), qs,
-                                          _ptr(scale), n_rows, k))
+    device = x.device
+    _on(device, q, scale)
+    _enqueue("i8_quantize_rows", _lib.i8_quantize_rows, device, x.data_ptr(), xt, xs, q.data_ptr(),
+             qs, scale.data_ptr(), n_rows, k)
     return q, scale
 
 
@@ -1006,13 +1015,13 @@ def i8_workspace(m, k, device):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _i8_operands(x, w, w_scale, x_scale, ws):
-    xt, xs = _rows(x, "x", _ACTS)
-    _, wst = _rows(w, "w", _INT8)
-    m, k = x.shape
-    if w.shape[1] != k:
-        raise ValueError(f"w: rows of {w.shape[1]} codes, x has {k}")
-    _vector(w_scale, w.shape[0], torch.float32, "w_scale")
+def _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated):
+    xt, xs, m, k = _rows(x, "x", _ACTS)
+    _, wst, rows, wk = _rows(w, "w", _INT8)
+    if wk != k:
+        raise ValueError(f"w: rows of {wk} codes, x has {k}")
+    _vector(w_scale, rows, torch.float32, "w_scale")
+    device = x.device
     if xt == 3:
         if x_scale is None:
             raise ValueError("x_scale: needed with int8 codes")
@@ -1021,9 +1030,27 @@ def _i8_operands(x, w, w_scale, x_scale, ws):
     else:
         if x_scale is not None:
             raise ValueError("x_scale: given with rows that are not int8 codes")
-        _need(ws, torch.uint8, "ws")
-    _one_device(x, w, w_scale, x_scale, ws)
-    return xt, xs, wst, m, k, ws
+        if ws is not None:
+            _need(ws, torch.uint8, "ws")
+    n = rows
+    if gated:
+        if rows % 2:
+            raise ValueError(f"w: {rows} rows, expected gate and up rows of one number")
+        n = rows // 2
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype, device=device)
+    yt, ys, y_rows, y_cols = _rows(out, "h" if gated else "y", _FLOATS)
+    if y_rows != m or y_cols != n:
+        raise ValueError(f"{'h' if gated else 'y'}: shape {(y_rows, y_cols)}, expected {(m, n)}")
+    if bias is not None:
+        _vector(bias, n, torch.float32, "bias")
+    _on(device, w, w_scale, x_scale, bias, out, ws)
+    _enqueue(name, fn, device, x.data_ptr(), xt, xs, None if x_scale is None else x_scale.data_ptr(),
+             w.data_ptr(), wst, w_scale.data_ptr(),
+             *(() if gated else (None if bias is None else bias.data_ptr(),)),
+             out.data_ptr(), yt, ys, n, k, m, None if ws is None else ws.data_ptr(),
+             0 if ws is None else ws.numel())
+    return out
 
 
 def i8_matmul(x, w, w_scale, x_scale=None, bias=None, y=None, dtype=torch.float32, ws=None):
@@ -1031,37 +1058,16 @@ def i8_matmul(x, w, w_scale, x_scale=None, bias=None, y=None, dtype=torch.float3
     x: int8 codes [m][k] with x_scale, or fp32 / fp16 / bf16 rows, quantized
     inside (ws: i8_workspace(m, k)); w: int8 [n][k]; w_scale, bias: fp32 [n].
     y: fp32, fp16 or bf16 [m][n] (made with `dtype` if not given)."""
-    xt, xs, wst, m, k, ws = _i8_operands(x, w, w_scale, x_scale, ws)
-    n = w.shape[0]
-    if y is None:
-        y = torch.empty((m, n), dtype=dtype, device=x.device)
-    yt, ys = _rows(y, "y", _FLOATS)
-    _shape(y, (m, n), "y")
-    _vector(bias, n, torch.float32, "bias")
-    _one_device(x, y, bias)
-    _check("i8_matmul", _on_device(
-        x, _lib.i8_matmul, _ptr(x), xt, xs, _ptr(x_scale), _ptr(w), wst, _ptr(w_scale), _ptr(bias),
-        _ptr(y), yt, ys, n, k, m, _ptr(ws), 0 if ws is None else ws.numel()))
-    return y
+    return _i8_product("i8_matmul", _lib.i8_matmul, x, w, w_scale, x_scale, bias, y, dtype, ws,
+                       False)
 
 
 def i8_up_gate_swiglu(x, w, w_scale, x_scale=None, h=None, dtype=torch.float32, ws=None):
     """h[t][j] = silu(g) * u with g, u the products of rows j and n_ff + j of
     the combined weight w int8 [2*n_ff][k] (gate rows first); x, x_scale, ws
     as for i8_matmul; h: fp32, fp16 or bf16 [m][n_ff]."""
-    xt, xs, wst, m, k, ws = _i8_operands(x, w, w_scale, x_scale, ws)
-    if w.shape[0] % 2:
-        raise ValueError(f"w: {w.shape[0]} rows, expected gate and up rows of one number")
-    n_ff = w.shape[0] // 2
-    if h is None:
-        h = torch.empty((m, n_ff), dtype=dtype, device=x.device)
-    ht, hs = _rows(h, "h", _FLOATS)
-    _shape(h, (m, n_ff), "h")
-    _one_device(x, h)
-    _check("i8_up_gate_swiglu", _on_device(
-        x, _lib.i8_up_gate_swiglu, _ptr(x), xt, xs, _ptr(x_scale), _ptr(w), wst, _ptr(w_scale),
-        _ptr(h), ht, hs, n_ff, k, m, _ptr(ws), 0 if ws is None else ws.numel()))
-    return h
+    return _i8_product("i8_up_gate_swiglu", _lib.i8_up_gate_swiglu, x, w, w_scale, x_scale, None, h,
+                       dtype, ws, True)
 
 
 class LogprobOut(NamedTuple):
@@ -1100,33 +1106,36 @@ def logprob_rows(logits, tokens=None, n_top=0, ws=None, out=None):
     of each row of logits, fp32 / fp16 / bf16 [m][n_vocab].  ws:
     logprob_workspace(m, n_vocab, n_top).  Returns a LogprobOut (`out` if
     given)."""
-    t, stride = _rows(logits, "logits", _FLOATS)
-    m, n_vocab = logits.shape
+    t, stride, m, n_vocab = _rows(logits, "logits", _FLOATS)
     if n_top < 0:
         raise Q8Error("logprob_rows", -2)
     n_given = 0
     if tokens is not None:
         _need(tokens, torch.int32, "tokens")
-        n_given = 1 if tokens.dim() == 1 else tokens.shape[-1]
-        if tokens.dim() not in (1, 2) or tokens.shape[0] != m:
-            raise ValueError(f"tokens: shape {tuple(tokens.shape)}, expected [{m}] or [{m}][n_given]")
+        shape = tokens.shape
+        if len(shape) not in (1, 2) or shape[0] != m:
+            raise ValueError(f"tokens: shape {tuple(shape)}, expected [{m}] or [{m}][n_given]")
+        n_given = 1 if len(shape) == 1 else shape[1]
+    device = logits.device
     if out is None:
-        out = logprob_outputs(m, n_given, n_top, logits.device)
+        out = logprob_outputs(m, n_given, n_top, device)
     logprob = out.logprob if n_given else None
     ids, top = (out.top_ids, out.top_logprobs) if n_top else (None, None)
     if (n_given and logprob is None) or (n_top and (ids is None or top is None)):
         raise ValueError("out: lacks an output that this call has")
-    _vector(logprob, m * n_given, torch.float32, "logprob")
+    if n_given:
+        _vector(logprob, m * n_given, torch.float32, "logprob")
     _vector(out.lse, m, torch.float32, "lse")
     _vector(out.entropy, m, torch.float32, "entropy")
-    _vector(ids, m * n_top, torch.int32, "top_ids")
-    _vector(top, m * n_top, torch.float32, "top_logprobs")
-    _need(ws, torch.uint8, "ws")
-    _one_device(logits, tokens, ws, *out)
-    _check("logprob_rows", _on_device(
-        logits, _lib.logprob_rows, _ptr(logits), t, stride, _ptr(tokens), n_given, _ptr(logprob),
-        _ptr(out.lse), _ptr(out.entropy), _ptr(ids), _ptr(top), m, n_vocab, n_top, _ptr(ws),
-        0 if ws is None else ws.numel()))
+    if n_top:
+        _vector(ids, m * n_top, torch.int32, "top_ids")
+        _vector(top, m * n_top, torch.float32, "top_logprobs")
+    if ws is not None:
+        _need(ws, torch.uint8, "ws")
+    _on(device, tokens, ws, *out)
+    _enqueue("logprob_rows", _lib.logprob_rows, device, logits.data_ptr(), t, stride, _ptr(tokens),
+             n_given, _ptr(logprob), out.lse.data_ptr(), out.entropy.data_ptr(), _ptr(ids), _ptr(top),
+             m, n_vocab, n_top, _ptr(ws), 0 if ws is None else ws.numel())
     return out
 
 

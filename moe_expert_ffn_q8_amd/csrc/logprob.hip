@@ -1,9 +1,18 @@
 // logprob.hip -- log probabilities of given tokens, log sum exp, entropy and the
-// largest logits of each row.
+// largest logits of each row, in one pass over the logits (HBM bounds it).
 //
-// One workgroup per row.  One pass keeps the running maximum M, S = sum
-// exp(x - M) and W = sum exp(x - M)(x - M); the top list is found one entry at
-// a time, each the largest (value, lowest index) below the last.
+// A workgroup takes a row, or a part of one where there are few rows; the parts
+// are joined by a second launch.  Every lane keeps a running (reference r, S =
+// sum 2^(x L - r L), W = sum 2^(x L - r L) (x L - r L)), L = log2 e, over 16-byte
+// loads, four in flight; per logit that is a fused multiply-add, an exponential,
+// two sums and a comparison.
+//
+// The largest n_top logits: every wave keeps candidates of its own, (value,
+// lowest index first) as one 64-bit key, in LDS, and the key that a logit has to
+// pass.  A wave starts from a bound -- the n_top-th largest of its lanes' first
+// maxima -- so few logits ever get in; when its 128 places are full, each
+// candidate counts the larger ones (its rank) and the first n_top stay.  Most
+// 16-byte groups are dismissed by their maximum, which the sums need anyway.
 #include "i8_device.h"
 #include "q8_i8.h"
 
@@ -11,126 +20,479 @@ namespace q8 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr float kL2E = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+constexpr int kPlaces = 128;      // candidates per wave
+constexpr int kMaxParts = 64;
+constexpr int kLoads = 4;         // 16-byte loads per lane and turn
 
-// Running (M, S, W).  M starts at the lowest finite value, so that x - M never
-// is infinity minus infinity for a row's -infinities; a NaN or +infinity makes
-// S NaN and stays.
+// r: the largest logit seen, or -1e38: x L stays finite beside it.
 struct Stat {
-    float m, s, w;
+    float r, s, w;
 };
 
-__device__ __forceinline__ Stat stat_zero() { return {-3.402823466e38f, 0.0f, 0.0f}; }
+__device__ __forceinline__ Stat stat_zero() { return {-1e38f, 0.0f, 0.0f}; }
 
-// The clamp keeps 0 * -infinity out of W; exp of it is 0 all the same.
-__device__ __forceinline__ float floor_d(float d) { return fmaxf(d, -1e30f); }
-
-__device__ __forceinline__ void stat_rescale(Stat &a, float m)
+__device__ __forceinline__ void stat_move(Stat &a, float r)
 {
-    const float d = floor_d(a.m - m), f = __expf(d);
-    a.w = (a.w + a.s * d) * f;
+    const float d = fmaxf(fmaf(a.r, kL2E, -(r * kL2E)), -1e30f);
+    const float f = __builtin_amdgcn_exp2f(d);
+    a.w = fmaf(a.s, d, a.w) * f;
     a.s *= f;
-    a.m = m;
-}
-
-__device__ __forceinline__ void stat_add(Stat &a, float x)
-{
-    if (x > a.m) stat_rescale(a, x);
-    const float d = x - a.m, e = __expf(d);
-    a.s += e;
-    a.w = fmaf(e, floor_d(d), a.w);
+    a.r = r;
 }
 
 __device__ __forceinline__ Stat stat_join(Stat a, Stat b)
 {
-    const float m = fmaxf(a.m, b.m);
-    stat_rescale(a, m);
-    stat_rescale(b, m);
-    return {m, a.s + b.s, a.w + b.w};
+    const float r = fmaxf(a.r, b.r);
+    stat_move(a, r);
+    stat_move(b, r);
+    return {r, a.s + b.s, a.w + b.w};
 }
 
-// Order of the top list: larger value first, then lower index; NaN last.
-__device__ __forceinline__ uint64_t order_key(float x, uint32_t i)
+__device__ __forceinline__ Stat wave_join(Stat st)
+{
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+        st = stat_join(st, {__shfl_xor(st.r, d), __shfl_xor(st.s, d), __shfl_xor(st.w, d)});
+    return st;
+}
+
+// Order of the top list: larger value first, then lower index; NaN last.  No
+// key of a logit is 0.
+__device__ __forceinline__ uint32_t value_key(float x)
 {
     const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);       // -0 -> +0
-    uint32_t key = (u >> 31) ? ~u : (u | 0x80000000u);
-    if (x != x) key = 0;
-    return ((uint64_t)key << 32) | (uint32_t)~i;
+    const uint32_t key = (u >> 31) ? ~u : (u | 0x80000000u);
+    return x != x ? 0u : key;
+}
+
+__device__ __forceinline__ uint64_t order_key(float x, uint32_t i)
+{
+    return ((uint64_t)value_key(x) << 32) | (uint32_t)~i;
+}
+
+__device__ __forceinline__ float key_value(uint64_t key)
+{
+    const uint32_t k = (uint32_t)(key >> 32);
+    if (k == 0) return __builtin_nanf("");
+    return __builtin_bit_cast(float, (k >> 31) ? (k & 0x7fffffffu) : ~k);
+}
+
+__device__ __forceinline__ int key_index(uint64_t key) { return (int)~(uint32_t)key; }
+
+// One wave's candidates.  thr: what a key has to exceed; least: a value below
+// which no logit can (-infinity: all have to be looked at).
+struct Top {
+    uint64_t *place;              // [kPlaces]
+    uint64_t thr;
+    float least;
+    int count, n;
+
+    __device__ __forceinline__ void init(uint64_t *p, int n_top)
+    {
+        place = p;
+        n = n_top;
+        count = 0;
+        set(0);
+    }
+    __device__ __forceinline__ void set(uint64_t t)
+    {
+        thr = t;
+        least = (t >> 32) > 0x007fffffu ? key_value(t) : -INFINITY;
+    }
+    // Ranks; the first n stay, in order.
+    __device__ __forceinline__ void compact(int lane)
+    {
+        if (lane == 0 && count < kPlaces) place[count] = 0;       // the pair read past the end
+        wave_lds_sync();
+        const uint64_t k0 = lane < count ? place[lane] : 0;
+        const uint64_t k1 = 64 + lane < count ? place[64 + lane] : 0;
+        int r0 = 0, r1 = 0;
+        for (int i = 0; i < count; i += 2) {
+            const ulonglong2 o = *(const ulonglong2 *)(place + i);
+            r0 += (o.x > k0) + (o.y > k0);
+            r1 += (o.x > k1) + (o.y > k1);
+        }
+        wave_lds_sync();
+        if (lane < count && r0 < n) place[r0] = k0;
+        if (64 + lane < count && r1 < n) place[r1] = k1;
+        wave_lds_sync();
+        if (count >= n) {
+            count = n;
+            const uint64_t t = place[n - 1];
+            set(((uint64_t)(uint32_t)wave_uniform((int)(t >> 32)) << 32) |
+                (uint32_t)wave_uniform((int)(uint32_t)t));
+        }
+    }
+    // One logit per lane (all lanes of the wave call).
+    __device__ __forceinline__ void offer(float x, uint32_t i, bool real, int lane)
+    {
+        const uint64_t key = order_key(x, i);
+        uint64_t in = __ballot(real && key > thr);
+        if (!in) return;
+        if (count + __popcll(in) > kPlaces) {
+            compact(lane);
+            in = __ballot(real && key > thr);
+        }
+        if (in >> lane & 1)
+            place[count + __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32),
+                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0))] = key;
+        count += __popcll(in);
+    }
+    // A first bound from one value key per lane (0: none): n lanes reach it.
+    __device__ __forceinline__ void bound(uint32_t lane_max)
+    {
+        uint32_t t = 0;
+        for (int b = 31; b >= 12; --b) {
+            const uint32_t c = t | (1u << b);
+            if (__popcll(__ballot(lane_max >= c)) >= n) t = c;
+        }
+        if (t) set(((uint64_t)t << 32) - 1);
+    }
+};
+
+struct Work {
+    Stat *stats;                  // [m][parts]
+    uint64_t *tops;               // [m][parts][n_top], 0 where a part has fewer
+    int parts;
+    int part_len;                 // logits, a multiple of 8
+};
+
+template <int T>
+__device__ __forceinline__ float logit(const LogprobArgs &a, int64_t row, int64_t i)
+{
+    return (float)((const typename Elem<T>::type *)a.logits)[row * a.row_stride + i];
+}
+
+// (r, S, W) of a whole row by one workgroup without the products x L, for the
+// rows where those overflow or nothing is finite: values at the ends of the
+// type's range, -infinity throughout, NaN, +infinity.  r is then the row's
+// maximum, S = 0 only if it is -infinity.
+template <int T>
+__device__ Stat slow_stat(const LogprobArgs &a, int64_t row, Stat *part, int waves)
+{
+    const int tid = threadIdx.x, n = 64 * waves;
+    float r = -INFINITY, bad = 0.0f;
+    for (int64_t i = tid; i < a.n_vocab; i += n) {
+        const float x = logit<T>(a, row, i);
+        r = fmaxf(r, x);
+        bad += x != x || x == INFINITY ? 1.0f : 0.0f;
+    }
+    for (int d = 32; d; d >>= 1) {
+        r = fmaxf(r, __shfl_xor(r, d));
+        bad += __shfl_xor(bad, d);
+    }
+    __syncthreads();
+    if ((tid & 63) == 0) part[tid >> 6] = {r, bad, 0.0f};
+    __syncthreads();
+    bad = 0.0f;
+    for (int w = 0; w < waves; ++w) {
+        r = fmaxf(r, part[w].r);
+        bad += part[w].s;
+    }
+    __syncthreads();
+    if (bad > 0.0f) return {r, __builtin_nanf(""), 0.0f};
+    if (r == -INFINITY) return {r, 0.0f, 0.0f};
+    Stat st = {r, 0.0f, 0.0f};
+    for (int64_t i = tid; i < a.n_vocab; i += n) {
+        const float d = fmaxf((logit<T>(a, row, i) - r) * kL2E, -1e30f);
+        const float e = __builtin_amdgcn_exp2f(d);
+        st.s += e;
+        st.w = fmaf(e, d, st.w);
+    }
+    for (int d = 32; d; d >>= 1) {
+        st.s += __shfl_xor(st.s, d);
+        st.w += __shfl_xor(st.w, d);
+    }
+    if ((tid & 63) == 0) part[tid >> 6] = st;
+    __syncthreads();
+    st = {r, 0.0f, 0.0f};
+    for (int w = 0; w < waves; ++w) {
+        st.s += part[w].s;
+        st.w += part[w].w;
+    }
+    return st;
+}
+
+// Outputs of a row from its (r, S, W), the same in every thread; `tops` are
+// `count` candidates in LDS, n_top of them the answer.
+template <int T>
+__device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stat st, Stat *part,
+                                       int waves, const uint64_t *tops, int count)
+{
+    const int tid = threadIdx.x, threads = 64 * waves;
+    float shift = 0.0f;                          // r L as rounded, minus r L
+    if (st.s > 0.0f && st.s < INFINITY)
+        shift = fmaf(-st.r, kL2E, st.r * kL2E);
+    else
+        st = slow_stat<T>(a, row, part, waves);
+    const bool empty = st.s == 0.0f;
+    const float l2 = log2f(st.s);
+    const float lse = empty ? -INFINITY : st.r + (l2 + shift) * kLn2;
+    if (tid == 0) {
+        if (a.lse) a.lse[row] = lse;
+        if (a.entropy) a.entropy[row] = empty ? 0.0f : (l2 - st.w / st.s) * kLn2;
+    }
+    auto lp = [&](float x) { return empty ? lse : x - lse; };
+    for (int i = tid; i < a.n_given; i += threads) {
+        const int64_t at = row * a.n_given + i;
+        const int tok = a.tokens[at];
+        a.logprob[at] = tok >= 0 && tok < a.n_vocab ? lp(logit<T>(a, row, tok)) : __builtin_nanf("");
+    }
+    for (int i = tid; i < count; i += threads) {
+        const uint64_t k = tops[i];
+        if (k == 0) continue;
+        int rank = 0;
+        for (int j = 0; j < count; j += 2) {
+            const ulonglong2 o = *(const ulonglong2 *)(tops + j);
+            rank += (o.x > k) + (o.y > k);
+        }
+        if (rank < a.n_top) {
+            a.top_ids[row * a.n_top + rank] = key_index(k);
+            a.top_logprobs[row * a.n_top + rank] = lp(key_value(k));
+        }
+    }
+}
+
+template <int T, int W, bool TOP>
+__global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, const Work wk)
+{
+    typedef typename Elem<T>::type E;
+    constexpr int V = kVec<T>;
+    static_assert(W % 2 == 0, "the lists together are whole pairs");
+    __shared__ Stat part[W];
+    __shared__ __align__(16) uint64_t places[TOP ? W : 1][TOP ? kPlaces : 2];
+    __shared__ __align__(16) uint64_t merged[TOP ? W * kLogprobMaxTop : 2];
+    const int64_t row = blockIdx.y;
+    const int lane = threadIdx.x & 63, wave = wave_uniform((int)(threadIdx.x >> 6));
+    const int begin = blockIdx.x * wk.part_len;
+    const int len = min(wk.part_len, (int)a.n_vocab - begin);
+    const E *x = (const E *)a.logits + row * a.row_stride + begin;
+    const int vecs = len / V, tail = len - vecs * V;
+
+    Stat st = stat_zero();
+    Top top;
+    if (TOP) top.init(places[wave], a.n_top);
+    bool first = TOP;
+    // a turn: kLoads x 64 vectors per wave; the logits past the last whole
+    // vector make one more, of one logit per lane
+    const int turn = 64 * kLoads;
+    for (int v0 = wave * turn; v0 < vecs + (tail > 0); v0 += W * turn) {
+        float xv[kLoads][V];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int v = v0 + 64 * u + lane;
+            u32x4 raw;
+            if (v < vecs)
+                __builtin_memcpy(&raw, x + (int64_t)v * V, 16);   // rows start at any element
+            else
+                raw = (u32x4){0u, 0u, 0u, 0u};
+            unpack16<T>(raw, xv[u]);
+        }
+        if (v0 + turn > vecs) {
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const int v = v0 + 64 * u + lane;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    if (v > vecs || (v == vecs && j >= tail))
+                        xv[u][j] = -INFINITY;
+                    else if (v == vecs)
+                        xv[u][j] = (float)x[vecs * V + j];
+                }
+            }
+        }
+        float best[kLoads], r = st.r;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            best[u] = xv[u][0];
+#pragma unroll
+            for (int j = 1; j < V; ++j) best[u] = fmaxf(best[u], xv[u][j]);
+            r = fmaxf(r, best[u]);
+        }
+        stat_move(st, r);
+        const float r2 = r * kL2E;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = fmaf(xv[u][j], kL2E, -r2);
+                const float e = __builtin_amdgcn_exp2f(d);
+                st.s += e;
+                st.w = fmaf(e, fmaxf(d, -1e30f), st.w);           // no 0 * infinity
+            }
+        if (TOP) {
+            if (first) {
+                uint32_t key = 0;
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int v = v0 + 64 * u + lane;
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (v < vecs) key = max(key, value_key(xv[u][j]));
+                }
+                top.bound(key);
+                first = false;
+            }
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                if (!__ballot(!(best[u] < top.least))) continue;
+                const int v = v0 + 64 * u + lane;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    if (!__ballot(!(xv[u][j] < top.least))) continue;
+                    top.offer(xv[u][j], (uint32_t)(begin + v * V + j),
+                              v < vecs || (v == vecs && j < tail), lane);
+                }
+            }
+        }
+    }
+
+    st = wave_join(st);
+    if (lane == 0) part[wave] = st;
+    if (TOP) {
+        top.compact(lane);
+        if (lane < a.n_top) merged[wave * a.n_top + lane] = lane < top.count ? top.place[lane] : 0;
+    }
+    __syncthreads();
+    st = part[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) st = stat_join(st, part[w]);
+    const int count = TOP ? W * a.n_top : 0;
+    if (wk.parts == 1) {
+        __syncthreads();
+        finish<T>(a, row, st, part, W, merged, count);
+        return;
+    }
+    const int64_t slot = row * wk.parts + blockIdx.x;
+    if (threadIdx.x == 0) wk.stats[slot] = st;
+    if (TOP) {
+        // the part's list: its entries by rank, 0 behind them
+        uint64_t *out = wk.tops + slot * a.n_top;
+        const int have = min(len, a.n_top);
+        for (int i = threadIdx.x; i < a.n_top; i += 64 * W)
+            if (i >= have) out[i] = 0;
+        for (int i = threadIdx.x; i < count; i += 64 * W) {
+            const uint64_t k = merged[i];
+            if (k == 0) continue;
+            int rank = 0;
+            for (int j = 0; j < count; j += 2) {
+                const ulonglong2 o = *(const ulonglong2 *)(merged + j);
+                rank += (o.x > k) + (o.y > k);
+            }
+            if (rank < a.n_top) out[rank] = k;
+        }
+    }
+}
+
+// The parts of a row.
+template <int T>
+__global__ __launch_bounds__(256) void logprob_join_kernel(const LogprobArgs a, const Work wk)
+{
+    __shared__ Stat part[4];
+    __shared__ __align__(16) uint64_t keys[kMaxParts * kLogprobMaxTop + 2];
+    __shared__ uint64_t least[4];
+    __shared__ int count;
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
+    Stat st = stat_zero();
+    if (lane < wk.parts) st = wk.stats[row * wk.parts + lane];
+    st = wave_join(st);
+    // the largest of the parts' last entries: n_top keys reach it
+    const uint64_t *tops = wk.tops + row * wk.parts * a.n_top;
+    if (a.n_top > 0) {
+        uint64_t t = lane < wk.parts ? tops[lane * a.n_top + a.n_top - 1] : 0;
+        for (int d = 32; d; d >>= 1) {
+            const uint64_t o = (uint64_t)__shfl_xor((long long)t, d);
+            t = o > t ? o : t;
+        }
+        if (tid == 0) {
+            least[0] = t;
+            count = 0;
+        }
+        __syncthreads();
+        t = least[0];
+        for (int i = tid; i < wk.parts * a.n_top; i += 256) {
+            const uint64_t k = tops[i];
+            if (k != 0 && k >= t) keys[atomicAdd(&count, 1)] = k;
+        }
+        __syncthreads();
+        if (tid == 0) keys[count] = 0;
+    }
+    __syncthreads();
+    finish<T>(a, row, st, part, 4, keys, a.n_top > 0 ? count : 0);
+}
+
+// How a call is cut: waves per workgroup and parts per row.
+struct Cut {
+    int waves, parts, part_len;
+};
+
+Cut cut(int64_t m, int64_t v)
+{
+    Cut c;
+    c.waves = 4;
+    int64_t parts = 1;
+    if (m < 1024) {
+        parts = (1024 + m - 1) / m;
+        if (parts > v / 4096) parts = v / 4096;
+        if (parts > kMaxParts) parts = kMaxParts;
+        if (parts < 1) parts = 1;
+    }
+    const int64_t len = ((v + parts - 1) / parts + 7) / 8 * 8;
+    c.part_len = (int)len;
+    c.parts = (int)((v + len - 1) / len);
+    return c;
 }
 
 template <int T>
-__global__ __launch_bounds__(kThreads) void logprob_kernel(const LogprobArgs a)
+int launch_type(const LogprobArgs &a, void *ws, hipStream_t stream)
 {
-    typedef typename Elem<T>::type E;
-    __shared__ Stat stats[kThreads / 64];
-    __shared__ uint64_t best[kThreads / 64];
-    __shared__ float result;
-    const int64_t row = blockIdx.x;
-    const E *x = (const E *)a.logits + row * a.row_stride;
-    const int v = (int)a.n_vocab;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    Stat st = stat_zero();
-    for (int i = tid; i < v; i += kThreads) stat_add(st, (float)x[i]);
-    for (int d = 32; d; d >>= 1)
-        st = stat_join(st, {__shfl_xor(st.m, d), __shfl_xor(st.s, d), __shfl_xor(st.w, d)});
-    if (lane == 0) stats[wave] = st;
-    __syncthreads();
-    if (tid == 0) {
-        for (int i = 1; i < kThreads / 64; ++i) st = stat_join(st, stats[i]);
-        const bool empty = st.s == 0.0f;
-        const float ls = logf(st.s);
-        const float lse = empty ? -INFINITY : st.m + ls;
-        if (a.lse) a.lse[row] = lse;
-        if (a.entropy) a.entropy[row] = empty ? 0.0f : ls - st.w / st.s;
-        result = lse;
+    const Cut c = cut(a.m, a.n_vocab);
+    Work wk;
+    wk.parts = c.parts;
+    wk.part_len = c.part_len;
+    wk.tops = (uint64_t *)ws;
+    wk.stats = (Stat *)(wk.tops + a.m * c.parts * a.n_top);
+    // rows are the grid's second axis: at most 65535 a launch
+    for (int64_t r0 = 0; r0 < a.m; r0 += 65535) {
+        const int64_t rows = a.m - r0 < 65535 ? a.m - r0 : 65535;
+        LogprobArgs b = a;
+        Work w = wk;
+        const int64_t es = T == Q8_T_F32 ? 4 : 2;
+        b.logits = (const uint8_t *)a.logits + r0 * a.row_stride * es;
+        if (a.n_given) { b.tokens += r0 * a.n_given; b.logprob += r0 * a.n_given; }
+        if (a.lse) b.lse += r0;
+        if (a.entropy) b.entropy += r0;
+        if (a.n_top) { b.top_ids += r0 * a.n_top; b.top_logprobs += r0 * a.n_top; }
+        b.m = rows;
+        w.tops += r0 * c.parts * a.n_top;
+        w.stats += r0 * c.parts;
+        const dim3 grid((unsigned)c.parts, (unsigned)rows), block(64 * c.waves);
+        if (a.n_top)
+            hipLaunchKernelGGL((logprob_kernel<T, 4, true>), grid, block, 0, stream, b, w);
+        else
+            hipLaunchKernelGGL((logprob_kernel<T, 4, false>), grid, block, 0, stream, b, w);
+        if (c.parts > 1)
+            hipLaunchKernelGGL(logprob_join_kernel<T>, dim3((unsigned)rows), dim3(256), 0, stream, b, w);
     }
-    __syncthreads();
-    const float lse = result;
-    // x - lse, with -infinity where the whole row is
-    auto lp = [&](float xv) { return lse == -INFINITY ? lse : xv - lse; };
-    for (int i = tid; i < a.n_given; i += kThreads) {
-        const int tok = a.tokens[row * a.n_given + i];
-        a.logprob[row * a.n_given + i] =
-            tok >= 0 && tok < v ? lp((float)x[tok]) : __builtin_nanf("");
-    }
-    uint64_t last = ~(uint64_t)0;
-    for (int n = 0; n < a.n_top; ++n) {
-        uint64_t b = 0;
-        for (int i = tid; i < v; i += kThreads) {
-            const uint64_t key = order_key((float)x[i], i);
-            if (key < last && key > b) b = key;
-        }
-        for (int d = 32; d; d >>= 1) {
-            const uint64_t o = (uint64_t)__shfl_xor((long long)b, d);
-            b = o > b ? o : b;
-        }
-        if (lane == 0) best[wave] = b;
-        __syncthreads();
-        for (int i = 0; i < kThreads / 64; ++i) b = best[i] > b ? best[i] : b;
-        __syncthreads();
-        last = b;
-        if (tid == 0) {
-            const uint32_t id = ~(uint32_t)b;
-            a.top_ids[row * a.n_top + n] = (int)id;
-            a.top_logprobs[row * a.n_top + n] = lp((float)x[id]);
-        }
-    }
+    return hipGetLastError() == hipSuccess ? 0 : -6;
 }
 
 }  // namespace
 
-size_t logprob_ws_bytes(int64_t, int64_t, int64_t) { return 0; }
-
-int launch_logprob(const LogprobArgs &a, void *, hipStream_t stream)
+size_t logprob_ws_bytes(int64_t m, int64_t n_vocab, int64_t n_top)
 {
-    const dim3 grid((unsigned)a.m), block(kThreads);
-    if (a.type == Q8_T_F32)
-        hipLaunchKernelGGL(logprob_kernel<Q8_T_F32>, grid, block, 0, stream, a);
-    else if (a.type == Q8_T_F16)
-        hipLaunchKernelGGL(logprob_kernel<Q8_T_F16>, grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL(logprob_kernel<Q8_T_BF16>, grid, block, 0, stream, a);
-    return hipGetLastError() == hipSuccess ? 0 : -6;
+    const Cut c = cut(m > 0 ? m : 1, n_vocab);
+    if (c.parts == 1) return 0;
+    return (size_t)m * c.parts * (8 * n_top + sizeof(Stat));
+}
+
+int launch_logprob(const LogprobArgs &a, void *ws, hipStream_t stream)
+{
+    if (a.type == Q8_T_F32) return launch_type<Q8_T_F32>(a, ws, stream);
+    if (a.type == Q8_T_F16) return launch_type<Q8_T_F16>(a, ws, stream);
+    return launch_type<Q8_T_BF16>(a, ws, stream);
 }
 
 }  // namespace q8
