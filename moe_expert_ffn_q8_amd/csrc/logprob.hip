@@ -9,10 +9,12 @@
 //
 // The largest n_top logits: every wave keeps candidates of its own, (value,
 // lowest index first) as one 64-bit key, in LDS, and the key that a logit has to
-// pass.  A wave starts from a bound -- the n_top-th largest of its lanes' first
-// maxima -- so few logits ever get in; when its 128 places are full, each
-// candidate counts the larger ones (its rank) and the first n_top stay.  Most
-// 16-byte groups are dismissed by their maximum, which the sums need anyway.
+// pass.  The workgroup starts from a common bound: with r = n_top / waves, the
+// (n_top / r)-th largest of the waves' r-th largest lane maxima over the first
+// turn (n_top logits reach it), so few logits ever get in.  When a wave's 128
+// places are full, each candidate counts the larger ones (its rank) and the
+// first n_top stay.  Most 16-byte groups are dismissed by their maximum, which
+// the sums need anyway.
 #include "i8_device.h"
 #include "q8_i8.h"
 
@@ -32,29 +34,60 @@ struct Stat {
 
 __device__ __forceinline__ Stat stat_zero() { return {-1e38f, 0.0f, 0.0f}; }
 
+// Both references as the rounded products that the terms were formed with (a
+// fused multiply-add would put the rounding of r L into every move, and at
+// -1e38 overflow the factor).
 __device__ __forceinline__ void stat_move(Stat &a, float r)
 {
-    const float d = fmaxf(fmaf(a.r, kL2E, -(r * kL2E)), -1e30f);
+    float d;
+    {
+#pragma clang fp contract(off)
+        const float old2 = a.r * kL2E, new2 = r * kL2E;
+        d = old2 - new2;
+    }
+    d = fmaxf(d, -1e30f);
     const float f = __builtin_amdgcn_exp2f(d);
     a.w = fmaf(a.s, d, a.w) * f;
     a.s *= f;
     a.r = r;
 }
 
-__device__ __forceinline__ Stat stat_join(Stat a, Stat b)
+// One term; r2 = the reference's product, a.r the reference.
+__device__ __forceinline__ void stat_add(Stat &a, float x, float r2)
 {
-    const float r = fmaxf(a.r, b.r);
-    stat_move(a, r);
-    stat_move(b, r);
-    return {r, a.s + b.s, a.w + b.w};
+    const float d = fmaf(x, kL2E, -r2);
+    const float e = __builtin_amdgcn_exp2f(d);
+    a.s += e;
+    a.w = fmaf(e, fmaxf(d, -1e30f), a.w);           // no 0 * infinity
+}
+
+// A reduction over the wave's lanes by data-parallel-primitive moves (in rows
+// of 16, then across them), the result in every lane.
+template <int Ctrl, int RowMask>
+__device__ __forceinline__ float dpp(float id, float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+        __builtin_bit_cast(int, id), __builtin_bit_cast(int, v), Ctrl, RowMask, 0xf, false));
+}
+
+template <bool MAX>
+__device__ __forceinline__ float wave_reduce(float v)
+{
+    const float id = MAX ? -INFINITY : 0.0f;
+    auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+    v = op(v, dpp<0x111, 0xf>(id, v));         // row_shr:1
+    v = op(v, dpp<0x112, 0xf>(id, v));         // row_shr:2
+    v = op(v, dpp<0x114, 0xf>(id, v));         // row_shr:4
+    v = op(v, dpp<0x118, 0xf>(id, v));         // row_shr:8
+    v = op(v, dpp<0x142, 0xa>(id, v));         // row_bcast:15
+    v = op(v, dpp<0x143, 0xc>(id, v));         // row_bcast:31
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 __device__ __forceinline__ Stat wave_join(Stat st)
 {
-#pragma unroll
-    for (int d = 32; d; d >>= 1)
-        st = stat_join(st, {__shfl_xor(st.r, d), __shfl_xor(st.s, d), __shfl_xor(st.w, d)});
-    return st;
+    stat_move(st, wave_reduce<true>(st.r));
+    return {st.r, wave_reduce<false>(st.s), wave_reduce<false>(st.w)};
 }
 
 // Order of the top list: larger value first, then lower index; NaN last.  No
@@ -79,6 +112,18 @@ __device__ __forceinline__ float key_value(uint64_t key)
 }
 
 __device__ __forceinline__ int key_index(uint64_t key) { return (int)~(uint32_t)key; }
+
+// The n-th largest of one key per lane, its low half cut (0: fewer than n
+// lanes have one).
+__device__ __forceinline__ uint32_t nth_key(uint32_t key, int n)
+{
+    uint32_t t = 0;
+    for (int b = 31; b >= 16; --b) {
+        const uint32_t c = t | (1u << b);
+        if (__popcll(__ballot(key >= c)) >= n) t = c;
+    }
+    return t;
+}
 
 // One wave's candidates.  thr: what a key has to exceed; least: a value below
 // which no logit can (-infinity: all have to be looked at).
@@ -139,15 +184,54 @@ struct Top {
                                                     __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0))] = key;
         count += __popcll(in);
     }
-    // A first bound from one value key per lane (0: none): n lanes reach it.
-    __device__ __forceinline__ void bound(uint32_t lane_max)
+};
+
+// Vectors with a logit that may get in, of one wave: a lane per logit looks at
+// them when there are 64 logits together.
+constexpr int kPend = 64 + 16;
+template <int T>
+struct Pending {
+    static constexpr int V = kVec<T>, kBatch = 64 / V;
+    u32x4 *vec;                   // [kPend]
+    int *at;
+    int count;
+
+    __device__ __forceinline__ void init(u32x4 *v, int *i)
     {
-        uint32_t t = 0;
-        for (int b = 31; b >= 12; --b) {
-            const uint32_t c = t | (1u << b);
-            if (__popcll(__ballot(lane_max >= c)) >= n) t = c;
+        vec = v;
+        at = i;
+        count = 0;
+    }
+    // vectors count .. count + n - 1, n <= kBatch
+    __device__ __forceinline__ void look(int n, int begin, Top &top, int lane) const
+    {
+        typedef typename Elem<T>::type E;
+        const int p = count + lane / V, j = lane % V;
+        const bool real = lane / V < n;
+        const float x = real ? (float)((const E *)(vec + p))[j] : -INFINITY;
+        top.offer(x, (uint32_t)(begin + (real ? at[p] : 0) * V + j), real, lane);
+    }
+    __device__ __forceinline__ void push(uint64_t in, u32x4 raw, int v, int begin, Top &top, int lane)
+    {
+        if (in >> lane & 1) {
+            const int p = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32),
+                                                            __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
+            vec[p] = raw;
+            at[p] = v;
         }
-        if (t) set(((uint64_t)t << 32) - 1);
+        count += __popcll(in);
+        wave_lds_sync();
+        while (count >= kBatch) {
+            count -= kBatch;
+            look(kBatch, begin, top, lane);
+        }
+        wave_lds_sync();
+    }
+    __device__ __forceinline__ void flush(int begin, Top &top, int lane)
+    {
+        const int n = count;
+        count = 0;
+        if (n) look(n, begin, top, lane);
     }
 };
 
@@ -259,10 +343,13 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
 {
     typedef typename Elem<T>::type E;
     constexpr int V = kVec<T>;
-    static_assert(W % 2 == 0, "the lists together are whole pairs");
     __shared__ Stat part[W];
     __shared__ __align__(16) uint64_t places[TOP ? W : 1][TOP ? kPlaces : 2];
-    __shared__ __align__(16) uint64_t merged[TOP ? W * kLogprobMaxTop : 2];
+    __shared__ __align__(16) uint64_t merged[TOP ? W * kLogprobMaxTop + 2 : 2];
+    __shared__ __align__(16) u32x4 pend_v[TOP ? W : 1][TOP ? kPend : 1];
+    __shared__ int pend_i[TOP ? W : 1][TOP ? kPend : 1];
+    __shared__ uint32_t bounds[W];
+    __shared__ int counts[W];
     const int64_t row = blockIdx.y;
     const int lane = threadIdx.x & 63, wave = wave_uniform((int)(threadIdx.x >> 6));
     const int begin = blockIdx.x * wk.part_len;
@@ -272,37 +359,34 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
 
     Stat st = stat_zero();
     Top top;
-    if (TOP) top.init(places[wave], a.n_top);
-    bool first = TOP;
-    // a turn: kLoads x 64 vectors per wave; the logits past the last whole
-    // vector make one more, of one logit per lane
+    Pending<T> pend;
+    if (TOP) {
+        top.init(places[wave], a.n_top);
+        pend.init(pend_v[wave], pend_i[wave]);
+    }
+    // a turn: kLoads x 64 vectors per wave
     const int turn = 64 * kLoads;
-    for (int v0 = wave * turn; v0 < vecs + (tail > 0); v0 += W * turn) {
-        float xv[kLoads][V];
+    for (int v0 = wave * turn; v0 == wave * turn || v0 < vecs; v0 += W * turn) {
+        u32x4 raw[kLoads];
+        float xv[kLoads][V], best[kLoads], r = st.r;
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-            const int v = v0 + 64 * u + lane;
-            u32x4 raw;
-            if (v < vecs)
-                __builtin_memcpy(&raw, x + (int64_t)v * V, 16);   // rows start at any element
+            // past the end the last vector again (none: 0), dismissed below
+            const int v = max(min(v0 + 64 * u + lane, vecs - 1), 0);
+            if (vecs > 0)
+                __builtin_memcpy(&raw[u], x + (int64_t)v * V, 16);   // rows start at any element
             else
-                raw = (u32x4){0u, 0u, 0u, 0u};
-            unpack16<T>(raw, xv[u]);
+                raw[u] = (u32x4){0u, 0u, 0u, 0u};
         }
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) unpack16<T>(raw[u], xv[u]);
         if (v0 + turn > vecs) {
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const int v = v0 + 64 * u + lane;
+            for (int u = 0; u < kLoads; ++u)
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (v > vecs || (v == vecs && j >= tail))
-                        xv[u][j] = -INFINITY;
-                    else if (v == vecs)
-                        xv[u][j] = (float)x[vecs * V + j];
-                }
-            }
+                for (int j = 0; j < V; ++j)
+                    if (v0 + 64 * u + lane >= vecs) xv[u][j] = -INFINITY;
         }
-        float best[kLoads], r = st.r;
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
             best[u] = xv[u][0];
@@ -315,52 +399,62 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = fmaf(xv[u][j], kL2E, -r2);
-                const float e = __builtin_amdgcn_exp2f(d);
-                st.s += e;
-                st.w = fmaf(e, fmaxf(d, -1e30f), st.w);           // no 0 * infinity
-            }
+            for (int j = 0; j < V; ++j) stat_add(st, xv[u][j], r2);
         if (TOP) {
-            if (first) {
-                uint32_t key = 0;
+            if (v0 == wave * turn) {               // the first turn, of every wave
+                float lane_max = __builtin_nanf("");
 #pragma unroll
-                for (int u = 0; u < kLoads; ++u) {
-                    const int v = v0 + 64 * u + lane;
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        if (v < vecs) key = max(key, value_key(xv[u][j]));
-                }
-                top.bound(key);
-                first = false;
+                for (int u = 0; u < kLoads; ++u)
+                    lane_max = fmaxf(lane_max, v0 + 64 * u + lane < vecs ? best[u] : __builtin_nanf(""));
+                const int each = (a.n_top + W - 1) / W;
+                const uint32_t mine = nth_key(value_key(lane_max), each);
+                if (lane == 0) bounds[wave] = mine;
+                __syncthreads();
+                const uint32_t all = nth_key(lane < W ? bounds[lane] : 0, (a.n_top + each - 1) / each);
+                if (all) top.set(((uint64_t)all << 32) - 1);
             }
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
-                if (!__ballot(!(best[u] < top.least))) continue;
                 const int v = v0 + 64 * u + lane;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    if (!__ballot(!(xv[u][j] < top.least))) continue;
-                    top.offer(xv[u][j], (uint32_t)(begin + v * V + j),
-                              v < vecs || (v == vecs && j < tail), lane);
-                }
+                const uint64_t in = __ballot(v < vecs && !(best[u] < top.least));
+                if (in) pend.push(in, raw[u], v, begin, top, lane);
             }
         }
+    }
+    if (TOP) pend.flush(begin, top, lane);
+    if (tail && wave == W - 1) {                   // the logits past the last vector
+        const float xt = lane < tail ? (float)x[vecs * V + lane] : -INFINITY;
+        const float r = fmaxf(st.r, xt);
+        stat_move(st, r);
+        stat_add(st, xt, r * kL2E);
+        if (TOP) top.offer(xt, (uint32_t)(begin + vecs * V + lane), lane < tail, lane);
     }
 
     st = wave_join(st);
     if (lane == 0) part[wave] = st;
     if (TOP) {
-        top.compact(lane);
-        if (lane < a.n_top) merged[wave * a.n_top + lane] = lane < top.count ? top.place[lane] : 0;
+        if (top.count > a.n_top) top.compact(lane);
+        wave_lds_sync();
+        if (lane == 0) counts[wave] = top.count;
     }
     __syncthreads();
-    st = part[0];
+    int count = 0;
+    if (TOP) {
+        // the waves' candidates behind each other, a 0 behind the last
+        int at = 0;
 #pragma unroll
-    for (int w = 1; w < W; ++w) st = stat_join(st, part[w]);
-    const int count = TOP ? W * a.n_top : 0;
+        for (int w = 0; w < W; ++w) {
+            if (w == wave) at = count;
+            count += counts[w];
+        }
+        for (int i = lane; i < top.count; i += 64) merged[at + i] = top.place[i];
+        if (threadIdx.x == 0) merged[count] = 0;
+    }
+    st = stat_zero();
+    if (lane < W) st = part[lane];
+    st = wave_join(st);
+    __syncthreads();
     if (wk.parts == 1) {
-        __syncthreads();
         finish<T>(a, row, st, part, W, merged, count);
         return;
     }
@@ -391,27 +485,20 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(const LogprobArgs a, 
 {
     __shared__ Stat part[4];
     __shared__ __align__(16) uint64_t keys[kMaxParts * kLogprobMaxTop + 2];
-    __shared__ uint64_t least[4];
     __shared__ int count;
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63;
     Stat st = stat_zero();
     if (lane < wk.parts) st = wk.stats[row * wk.parts + lane];
     st = wave_join(st);
-    // the largest of the parts' last entries: n_top keys reach it
+    // a bound from the parts' r-th entries, as in the first turn of a part
     const uint64_t *tops = wk.tops + row * wk.parts * a.n_top;
     if (a.n_top > 0) {
-        uint64_t t = lane < wk.parts ? tops[lane * a.n_top + a.n_top - 1] : 0;
-        for (int d = 32; d; d >>= 1) {
-            const uint64_t o = (uint64_t)__shfl_xor((long long)t, d);
-            t = o > t ? o : t;
-        }
-        if (tid == 0) {
-            least[0] = t;
-            count = 0;
-        }
+        const int each = (a.n_top + wk.parts - 1) / wk.parts;
+        const uint64_t last = lane < wk.parts ? tops[lane * a.n_top + each - 1] : 0;
+        const uint64_t t = (uint64_t)nth_key((uint32_t)(last >> 32), (a.n_top + each - 1) / each) << 32;
+        if (tid == 0) count = 0;
         __syncthreads();
-        t = least[0];
         for (int i = tid; i < wk.parts * a.n_top; i += 256) {
             const uint64_t k = tops[i];
             if (k != 0 && k >= t) keys[atomicAdd(&count, 1)] = k;
@@ -431,18 +518,29 @@ struct Cut {
 Cut cut(int64_t m, int64_t v)
 {
     Cut c;
-    c.waves = 4;
-    int64_t parts = 1;
-    if (m < 1024) {
-        parts = (1024 + m - 1) / m;
-        if (parts > v / 4096) parts = v / 4096;
-        if (parts > kMaxParts) parts = kMaxParts;
-        if (parts < 1) parts = 1;
-    }
+    c.waves = v > 8192 && m < 256 ? 16 : 4;
+    int64_t parts = (512 + m - 1) / (m > 0 ? m : 1);
+    if (parts > v / 16384) parts = v / 16384;
+    if (parts > kMaxParts) parts = kMaxParts;
+    if (parts < 1) parts = 1;
     const int64_t len = ((v + parts - 1) / parts + 7) / 8 * 8;
     c.part_len = (int)len;
     c.parts = (int)((v + len - 1) / len);
     return c;
+}
+
+template <int T>
+void launch_part(const LogprobArgs &a, const Work &w, const Cut &c, hipStream_t stream)
+{
+    const dim3 grid((unsigned)c.parts, (unsigned)a.m), block(64 * c.waves);
+    if (c.waves == 4 && a.n_top)
+        hipLaunchKernelGGL((logprob_kernel<T, 4, true>), grid, block, 0, stream, a, w);
+    else if (c.waves == 4)
+        hipLaunchKernelGGL((logprob_kernel<T, 4, false>), grid, block, 0, stream, a, w);
+    else if (a.n_top)
+        hipLaunchKernelGGL((logprob_kernel<T, 16, true>), grid, block, 0, stream, a, w);
+    else
+        hipLaunchKernelGGL((logprob_kernel<T, 16, false>), grid, block, 0, stream, a, w);
 }
 
 template <int T>
@@ -468,11 +566,7 @@ int launch_type(const LogprobArgs &a, void *ws, hipStream_t stream)
         b.m = rows;
         w.tops += r0 * c.parts * a.n_top;
         w.stats += r0 * c.parts;
-        const dim3 grid((unsigned)c.parts, (unsigned)rows), block(64 * c.waves);
-        if (a.n_top)
-            hipLaunchKernelGGL((logprob_kernel<T, 4, true>), grid, block, 0, stream, b, w);
-        else
-            hipLaunchKernelGGL((logprob_kernel<T, 4, false>), grid, block, 0, stream, b, w);
+        launch_part<T>(b, w, c, stream);
         if (c.parts > 1)
             hipLaunchKernelGGL(logprob_join_kernel<T>, dim3((unsigned)rows), dim3(256), 0, stream, b, w);
     }
