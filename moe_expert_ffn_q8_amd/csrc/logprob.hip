@@ -9,11 +9,11 @@
 //
 // The largest n_top logits: every wave keeps candidates of its own, (value,
 // lowest index first) as one 64-bit key, in LDS, and the key that a logit has to
-// pass.  The workgroup starts from a common bound: with r = n_top / waves, the
-// (n_top / r)-th largest of the waves' r-th largest lane maxima over the first
-// turn (n_top logits reach it), so few logits ever get in.  When a wave's 128
-// places are full, each candidate counts the larger ones (its rank) and the
-// first n_top stay.  Most 16-byte groups are dismissed by their maximum, which
+// pass.  After turns 1, 2, 4, 8, ... the workgroup sets a common bound: with r =
+// n_top / waves, the (n_top / r)-th largest of the waves' r-th largest lane
+// maxima so far (n_top logits reach it), so few logits ever get in.  When a
+// wave's 128 places are full, each candidate counts the larger ones (its rank)
+// and the first n_top stay.  Most 16-byte groups are dismissed by their maximum, which
 // the sums need anyway.
 #include "i8_device.h"
 #include "q8_i8.h"
@@ -248,6 +248,25 @@ __device__ __forceinline__ float logit(const LogprobArgs &a, int64_t row, int64_
     return (float)((const typename Elem<T>::type *)a.logits)[row * a.row_stride + i];
 }
 
+// The 16 bytes that unpack16 took the values from.
+template <int T>
+__device__ __forceinline__ u32x4 repack16(const float (&v)[kVec<T>])
+{
+    uint32_t d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (T == Q8_T_F32)
+            d[i] = __builtin_bit_cast(uint32_t, v[i]);
+        else if constexpr (T == Q8_T_F16)
+            d[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * i]) |
+                   (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * i + 1]) << 16;
+        else
+            d[i] = __builtin_bit_cast(uint32_t, v[2 * i]) >> 16 |
+                   (__builtin_bit_cast(uint32_t, v[2 * i + 1]) & 0xffff0000u);
+    }
+    return (u32x4){d[0], d[1], d[2], d[3]};
+}
+
 // (r, S, W) of a whole row by one workgroup without the products x L, for the
 // rows where those overflow or nothing is finite: values at the ends of the
 // type's range, -infinity throughout, NaN, +infinity.  r is then the row's
@@ -348,14 +367,18 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
     __shared__ __align__(16) uint64_t merged[TOP ? W * kLogprobMaxTop + 2 : 2];
     __shared__ __align__(16) u32x4 pend_v[TOP ? W : 1][TOP ? kPend : 1];
     __shared__ int pend_i[TOP ? W : 1][TOP ? kPend : 1];
-    __shared__ uint32_t bounds[W];
+    __shared__ uint32_t bounds[2][W];
     __shared__ int counts[W];
     const int64_t row = blockIdx.y;
     const int lane = threadIdx.x & 63, wave = wave_uniform((int)(threadIdx.x >> 6));
     const int begin = blockIdx.x * wk.part_len;
     const int len = min(wk.part_len, (int)a.n_vocab - begin);
-    const E *x = (const E *)a.logits + row * a.row_stride + begin;
-    const int vecs = len / V, tail = len - vecs * V;
+    const E *x0 = (const E *)a.logits + row * a.row_stride + begin;
+    // whole 16-byte vectors from the first aligned one; the logits before and
+    // after them (up to 14) are taken one per lane at the end
+    const int head = min((int)((-(uintptr_t)x0 & 15) / sizeof(E)), len);
+    const E *x = x0 + head;
+    const int vecs = (len - head) / V, tail = len - head - vecs * V;
 
     Stat st = stat_zero();
     Top top;
@@ -364,22 +387,27 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
         top.init(places[wave], a.n_top);
         pend.init(pend_v[wave], pend_i[wave]);
     }
-    // a turn: kLoads x 64 vectors per wave
+    // a turn: kLoads x 64 vectors per wave; every wave makes the same number
     const int turn = 64 * kLoads;
-    for (int v0 = wave * turn; v0 == wave * turn || v0 < vecs; v0 += W * turn) {
-        u32x4 raw[kLoads];
-        float xv[kLoads][V], best[kLoads], r = st.r;
+    u32x4 raw[kLoads];
+    auto fetch = [&](int v0) {
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-            // past the end the last vector again (none: 0), dismissed below
-            const int v = max(min(v0 + 64 * u + lane, vecs - 1), 0);
-            if (vecs > 0)
-                __builtin_memcpy(&raw[u], x + (int64_t)v * V, 16);   // rows start at any element
-            else
-                raw[u] = (u32x4){0u, 0u, 0u, 0u};
+            // past the end the last vector again, dismissed below
+            const int v = min(v0 + 64 * u + lane, vecs - 1);
+            raw[u] = __builtin_nontemporal_load((const u32x4 *)(x + (int64_t)v * V));
         }
+    };
+    const int edge_i = lane < head ? lane : lane + vecs * V;
+    const float edge = lane < head + tail && wave == W - 1 ? (float)x0[edge_i] : -INFINITY;
+    if (vecs > 0) fetch(wave * turn);
+    float lane_max = __builtin_nanf("");
+    for (int it = 0; it * W * turn < vecs; ++it) {
+        const int v0 = (it * W + wave) * turn;
+        float xv[kLoads][V], best[kLoads], r = st.r;
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) unpack16<T>(raw[u], xv[u]);
+        if ((it + 1) * W * turn < vecs) fetch(v0 + W * turn);    // lands during this turn
         if (v0 + turn > vecs) {
 #pragma unroll
             for (int u = 0; u < kLoads; ++u)
@@ -401,33 +429,36 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
 #pragma unroll
             for (int j = 0; j < V; ++j) stat_add(st, xv[u][j], r2);
         if (TOP) {
-            if (v0 == wave * turn) {               // the first turn, of every wave
-                float lane_max = __builtin_nanf("");
 #pragma unroll
-                for (int u = 0; u < kLoads; ++u)
-                    lane_max = fmaxf(lane_max, v0 + 64 * u + lane < vecs ? best[u] : __builtin_nanf(""));
-                const int each = (a.n_top + W - 1) / W;
+            for (int u = 0; u < kLoads; ++u)
+                lane_max = fmaxf(lane_max, v0 + 64 * u + lane < vecs ? best[u] : __builtin_nanf(""));
+            if ((it & (it + 1)) == 0) {            // turns 1, 2, 4, 8, ...
+                // waves that have had a whole turn, or the first
+                const int full = max(min(vecs / turn, W), 1);
+                const int each = (a.n_top + full - 1) / full;
                 const uint32_t mine = nth_key(value_key(lane_max), each);
-                if (lane == 0) bounds[wave] = mine;
+                // (a wave is at most one barrier ahead: two sets are enough)
+                uint32_t *set = bounds[__builtin_popcount(it) & 1];
+                if (lane == 0) set[wave] = mine;
                 __syncthreads();
-                const uint32_t all = nth_key(lane < W ? bounds[lane] : 0, (a.n_top + each - 1) / each);
-                if (all) top.set(((uint64_t)all << 32) - 1);
+                const uint32_t all = nth_key(lane < W ? set[lane] : 0, (a.n_top + each - 1) / each);
+                const uint64_t t = ((uint64_t)all << 32) - 1;
+                if (all && t > top.thr) top.set(t);
             }
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 const int v = v0 + 64 * u + lane;
                 const uint64_t in = __ballot(v < vecs && !(best[u] < top.least));
-                if (in) pend.push(in, raw[u], v, begin, top, lane);
+                if (in) pend.push(in, repack16<T>(xv[u]), v, begin + head, top, lane);
             }
         }
     }
-    if (TOP) pend.flush(begin, top, lane);
-    if (tail && wave == W - 1) {                   // the logits past the last vector
-        const float xt = lane < tail ? (float)x[vecs * V + lane] : -INFINITY;
-        const float r = fmaxf(st.r, xt);
+    if (TOP) pend.flush(begin + head, top, lane);
+    if (head + tail && wave == W - 1) {
+        const float r = fmaxf(st.r, edge);
         stat_move(st, r);
-        stat_add(st, xt, r * kL2E);
-        if (TOP) top.offer(xt, (uint32_t)(begin + vecs * V + lane), lane < tail, lane);
+        stat_add(st, edge, r * kL2E);
+        if (TOP) top.offer(edge, (uint32_t)(begin + edge_i), lane < head + tail, lane);
     }
 
     st = wave_join(st);
@@ -518,11 +549,15 @@ struct Cut {
 Cut cut(int64_t m, int64_t v)
 {
     Cut c;
-    c.waves = v > 8192 && m < 256 ? 16 : 4;
-    int64_t parts = (512 + m - 1) / (m > 0 ? m : 1);
+    // 1024 workgroups of 4 waves fill the device; from 512 rows on a second
+    // launch costs more than it gives (512 x 262144 bf16: 42 us in one, 46 in
+    // two parts; 300 rows: 37 and 33 us)
+    int64_t parts = m >= 512 ? 1 : 1024 / (m > 0 ? m : 1);
     if (parts > v / 16384) parts = v / 16384;
     if (parts > kMaxParts) parts = kMaxParts;
     if (parts < 1) parts = 1;
+    // fewer workgroups than CUs: more waves each
+    c.waves = m * parts < 256 && v > 8192 ? 16 : 4;
     const int64_t len = ((v + parts - 1) / parts + 7) / 8 * 8;
     c.part_len = (int)len;
     c.parts = (int)((v + len - 1) / len);
