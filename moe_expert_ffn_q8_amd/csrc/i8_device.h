@@ -111,14 +111,53 @@ __device__ __forceinline__ float silu_mul(float g, float u)
     return g * __builtin_amdgcn_rcpf(d) * u;
 }
 
-// One value, rounded to nearest even to the output's type.  (The value is
-// pinned as fp32 first: a last product merged with the conversion, as
-// v_fma_mixlo_f16 does, would round once where another kernel rounds twice.)
+// A value rounded to nearest even to the output's type.  (It is pinned as fp32
+// first: a last product merged with the conversion, as v_fma_mixlo_f16 does,
+// would round once where another kernel rounds twice.)
+template <int T>
+__device__ __forceinline__ typename Elem<T>::type round_out(float v)
+{
+    if constexpr (T == Q8_T_F16) asm("" : "+v"(v));
+    return (typename Elem<T>::type)v;
+}
+
 template <int T>
 __device__ __forceinline__ void store_out(void *y, int64_t i, float v)
 {
-    if constexpr (T == Q8_T_F16) asm("" : "+v"(v));
-    ((typename Elem<T>::type *)y)[i] = (typename Elem<T>::type)v;
+    ((typename Elem<T>::type *)y)[i] = round_out<T>(v);
+}
+
+// Two values of a 16-bit type in a dword.
+template <int T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if constexpr (T == Q8_T_F32) return 0;
+    else
+        return (uint32_t)__builtin_bit_cast(uint16_t, round_out<T>(lo)) |
+               (uint32_t)__builtin_bit_cast(uint16_t, round_out<T>(hi)) << 16;
+}
+
+// 16 bytes of outputs at element i, the first `left` elements of them (element
+// alignment is enough).
+template <int T>
+__device__ __forceinline__ void store16(void *y, int64_t i, u32x4 v, int left)
+{
+    typedef typename Elem<T>::type E;
+    typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+    constexpr int V = kVec<T>;
+    if (left >= V) {
+        *(u32x4_any *)((E *)y + i) = v;
+        return;
+    }
+    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int r = 0; r < V - 1; ++r) {
+        if (r >= left) break;
+        if constexpr (T == Q8_T_F32)
+            ((uint32_t *)y)[i + r] = d[r];
+        else
+            ((uint16_t *)y)[i + r] = (uint16_t)(d[r / 2] >> (16 * (r & 1)));
+    }
 }
 
 // Up to 4 consecutive values.

@@ -12,12 +12,12 @@
 //    computes NI x MI tiles of 32 x 32.  In the gated form half of a wave's
 //    weight rows are gate rows and the other half the up rows of the same
 //    outputs, so that silu(g) * u is formed in registers.
-//  * k is walked in steps of 128 bytes.  A step of both operands goes straight
+//  * k is walked in steps of 64 bytes.  A step of both operands goes straight
 //    from HBM to LDS (16-byte buffer loads in LDS DMA mode; rows past m or n
-//    and bytes past k read as zero), double-buffered: the loads of step s + 2
-//    go out when the last fragments of step s are in registers and have a
-//    whole step to land.
-//  * A staged row is 128 bytes, its 16-byte chunk c at slot c ^ ((row/2) % 8):
+//    and bytes past k read as zero) into a ring of kStages stages: the loads of
+//    step s + kStages go out when the last fragments of step s are in
+//    registers, and kStages - 1 steps pass before they are waited for.
+//  * A staged row is 64 bytes, its 16-byte chunk c at slot c ^ ((row/4) % 4):
 //    the 16-byte fragment reads of 16 consecutive rows then fall on all 64
 //    banks once, and the swizzle costs nothing (the DMA's LDS side is linear,
 //    the lanes' global addresses carry it).
@@ -36,9 +36,10 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 
-constexpr int kStep = 128;        // bytes of k per step
+constexpr int kStep = 64;         // bytes of k per step
+constexpr int kStages = 5;        // 160 KB of LDS at 256 x 256
 constexpr int kGroupM = 8;        // token tiles next to each other
-constexpr int kOut = 0x7fffff00;  // an offset past every resource: reads zero
+constexpr int kOut = 0x7ff00000;  // an offset past every resource: reads zero
 
 struct TileGrid {
     int tiles_n, tiles_m;
@@ -49,13 +50,18 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
 {
     constexpr int kWaves = WN * WM;
     constexpr int NI = TN / WN / 32, MI = TM / WM / 32;
-    constexpr int kLoadsW = TN / 8 / kWaves, kLoadsX = TM / 8 / kWaves;
+    constexpr int kLoadsW = TN / 16 / kWaves, kLoadsX = TM / 16 / kWaves;
     constexpr int kCols = GATED ? TN / 2 : TN;          // outputs per tile
     constexpr int kWaveCols = kCols / WN;
-    static_assert(TN % (8 * kWaves) == 0 && TM % (8 * kWaves) == 0, "whole loads per wave");
+    static_assert(TN % (16 * kWaves) == 0 && TM % (16 * kWaves) == 0, "whole loads per wave");
     static_assert(!GATED || NI % 2 == 0, "gate and up halves");
+    // separate objects: a fragment read then waits for its own stage's loads
     __shared__ __align__(16) uint8_t stage0[(TN + TM) * kStep];
     __shared__ __align__(16) uint8_t stage1[(TN + TM) * kStep];
+    __shared__ __align__(16) uint8_t stage2[(TN + TM) * kStep];
+    __shared__ __align__(16) uint8_t stage3[(TN + TM) * kStep];
+    __shared__ __align__(16) uint8_t stage4[(TN + TM) * kStep];
+    static_assert(kStages == 5, "stage0 .. stage4");
 
     const int wave = wave_uniform((int)(threadIdx.x >> 6));
     const int lane = threadIdx.x & 63;
@@ -80,13 +86,12 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
         (void *)(a.x + m0 * a.x_stride), 0, (x_rows - 1) * x_stride + k, kBufferWord3);
     const int8_t *w_base[kLoadsW];     // (no array of resources: the host pass has no such type)
     int voff[kLoadsW + kLoadsX];
-    // load u of a wave: staged rows 8f .. 8f+7, f = wave + kWaves * u
-    const int lr = lane >> 3;
-    const int chunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);   // (8f + lr)/2 % 8
-    static_assert(kWaves % 2 == 0, "the chunk of a lane is the same for every load");
+    // load u of a wave: staged rows 16f .. 16f+15, f = wave + kWaves * u
+    const int lr = lane >> 2;
+    const int chunk = (lane & 3) ^ (lane >> 4);
 #pragma unroll
     for (int u = 0; u < kLoadsW; ++u) {
-        const int b = 8 * (wave + kWaves * u);          // of TN; 32-row groups are uniform
+        const int b = 16 * (wave + kWaves * u);         // of TN; 32-row groups are uniform
         int row = b;
         const int8_t *base = a.w + n0 * a.w_stride;
         if (GATED) {
@@ -99,17 +104,17 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
     }
 #pragma unroll
     for (int u = 0; u < kLoadsX; ++u) {
-        const int row = 8 * (wave + kWaves * u) + lr;
+        const int row = 16 * (wave + kWaves * u) + lr;
         voff[kLoadsW + u] = row < x_rows ? row * x_stride + 16 * chunk : kOut;
     }
 
     auto issue = [&](int st, uint8_t *s) {
         const bool in_k = 16 * chunk < k - st * kStep;
-        const int so = st * kStep;
+        const int so = min(st * kStep, k);       // (kOut + so stays below 2^31)
 #pragma unroll
         for (int u = 0; u < kLoadsW + kLoadsX; ++u) {
             const int off = in_k ? voff[u] : kOut;
-            const int f = u < kLoadsW ? wave + kWaves * u : TN / 8 + wave + kWaves * (u - kLoadsW);
+            const int f = u < kLoadsW ? wave + kWaves * u : TN / 16 + wave + kWaves * (u - kLoadsW);
             auto *dst = (__attribute__((address_space(3))) void *)(s + 1024 * f);
             if (u < kLoadsW) {
                 const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
@@ -119,6 +124,24 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, dst, 16, off, so, 0, 0);
         }
     };
+
+    // what the outputs need: one weight row's scale and bias per thread, the
+    // scales of the lane's tokens
+    const int tid = threadIdx.x;
+    float w_scale = 0.0f, w_bias = 0.0f, s_x[MI];
+    static_assert(TN <= 64 * kWaves, "a thread per weight row");
+    if (tid < TN) {
+        const int grp = tid / 32 % NI;
+        const int64_t col = n0 + (GATED ? tid / (32 * NI) * kWaveCols + 32 * (grp % (NI / 2 + !GATED)) + tid % 32
+                                        : tid);
+        if (col < a.n) {
+            w_scale = a.w_scale[GATED && grp >= NI / 2 ? a.n + col : col];
+            if (!GATED && a.bias) w_bias = a.bias[col];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < MI; ++j)
+        s_x[j] = a.x_scale[min(m0 + (wm * MI + j) * 32 + li, a.m - 1)];
 
     v16i acc[NI][MI];
 #pragma unroll
@@ -133,7 +156,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
     };
     // 32 bytes of k (k-group s of the step): lane = row li, bytes 16h .. 16h+15
     const int row_w = (wn * NI * 32 + li) * kStep, row_x = (TN + wm * MI * 32 + li) * kStep;
-    const int swz = (li >> 1) & 7;
+    const int swz = (li >> 2) & 3;
     auto load = [&](const uint8_t *s, int ks, Frag &f) {
         const int c = 16 * ((2 * ks + h) ^ swz);
 #pragma unroll
@@ -148,55 +171,110 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
             for (int j = 0; j < MI; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[i], f.x[j], acc[i][j], 0, 0, 0);
     };
-    auto landed = [&]() {
-        __builtin_amdgcn_s_waitcnt(0x3f70);    // vmcnt(0): this wave's loads are in LDS
-        __syncthreads();
+    // this wave's loads of the next stage have landed and its reads of this one
+    // are done; then every wave's (a __syncthreads would wait for the later
+    // stages' loads too)
+    auto next_stage = [&]() {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kStages - 2) * (kLoadsW + kLoadsX)) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
     };
 
     const int steps = (k + kStep - 1) / kStep;
     Frag f0, f1;
     issue(0, stage0);
-    if (steps > 1) issue(1, stage1);
-    landed();
+    issue(1, stage1);
+    issue(2, stage2);
+    issue(3, stage3);
+    issue(4, stage4);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 1) * (kLoadsW + kLoadsX)) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
     load(stage0, 0, f0);
+    // a step past the end loads zeros, so that every wait count is exact
     auto body = [&](int st, uint8_t *cur, const uint8_t *next) {
         load(cur, 1, f1);
         mul(f0);
-        load(cur, 2, f0);
-        mul(f1);
-        load(cur, 3, f1);
-        mul(f0);
-        landed();                              // and every wave is done reading cur
-        if (st + 2 < steps) issue(st + 2, cur);
-        if (st + 1 < steps) load(next, 0, f0);
+        next_stage();
+        issue(st + kStages, cur);
+        load(next, 0, f0);
         mul(f1);
     };
-    for (int st = 0; st < steps; st += 2) {
+    int st = 0;
+    for (; st + kStages <= steps; st += kStages) {
         body(st, stage0, stage1);
-        if (st + 1 < steps) body(st + 1, stage1, stage0);
+        body(st + 1, stage1, stage2);
+        body(st + 2, stage2, stage3);
+        body(st + 3, stage3, stage4);
+        body(st + 4, stage4, stage0);
     }
+    if (st < steps) body(st, stage0, stage1);
+    if (st + 1 < steps) body(st + 1, stage1, stage2);
+    if (st + 2 < steps) body(st + 2, stage2, stage3);
+    if (st + 3 < steps) body(st + 3, stage3, stage4);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (zeros still on their way to LDS)
 
-    // result r of a lane: weight row 8(r/4) + 4h + r%4 of its tile, token li
+    // Outputs.  Result r of a lane: weight row 8(r/4) + 4h + r%4 of its tile,
+    // token li.  The tile's scales (and bias) go to LDS, and every wave turns its
+    // results round there, 32 tokens x 128 bytes at a time (swizzled as above), so
+    // that a token's outputs leave as runs of 16-byte stores.
+    __syncthreads();                           // every wave is done with the stages
+    float *scales = (float *)stage1;           // [TN], then bias [TN]
+    if (tid < TN) {
+        scales[tid] = w_scale;
+        if (!GATED) scales[TN + tid] = w_bias;
+    }
+    __syncthreads();
+    constexpr int kES = YT == Q8_T_F32 ? 4 : 2;
+    constexpr int kOutTiles = GATED ? NI / 2 : NI;
+    constexpr int kPass = kOutTiles < 4 / kES ? kOutTiles : 4 / kES;    // tiles side by side
+    constexpr int kChunks = kPass * 32 * kES / 16;                      // 16-byte pieces a row
+    uint8_t *turn = stage0 + wave * 4096;
+    static_assert(kWaves * 4096 <= (TN + TM) * kStep && TN * 8 <= (TN + TM) * kStep, "fits");
+    const bool biased = !GATED && a.bias;
 #pragma unroll
     for (int j = 0; j < MI; ++j) {
-        const int64_t t = m0 + (wm * MI + j) * 32 + li;
-        if (t >= a.m) continue;
-        const float sx = a.x_scale[t];
 #pragma unroll
-        for (int i = 0; i < (GATED ? NI / 2 : NI); ++i)
+        for (int i0 = 0; i0 < kOutTiles; i0 += kPass) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int64_t n = n0 + wn * kWaveCols + 32 * i + 8 * (r / 4) + 4 * h + r % 4;
-                if (n >= a.n) continue;
-                float v;
-                if (GATED)
-                    v = silu_mul(i8_rescale(acc[i][j][r], sx, a.w_scale[n]),
-                                 i8_rescale(acc[i + NI / 2][j][r], sx, a.w_scale[a.n + n]));
-                else
-                    v = a.bias ? i8_rescale(acc[i][j][r], sx, a.w_scale[n], a.bias[n])
-                               : i8_rescale(acc[i][j][r], sx, a.w_scale[n]);
-                store_out<YT>(a.y, t * a.y_stride + n, v);
+            for (int ip = 0; ip < kPass; ++ip)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i = i0 + ip, row = (wn * NI + i) * 32 + 8 * q + 4 * h;
+                    const float4 sg = *(const float4 *)(scales + row);
+                    float4 su = sg, sb = sg;
+                    if (GATED) su = *(const float4 *)(scales + row + NI / 2 * 32);
+                    if (!GATED) sb = *(const float4 *)(scales + TN + row);
+                    const float g4[4] = {sg.x, sg.y, sg.z, sg.w}, u4[4] = {su.x, su.y, su.z, su.w},
+                                b4[4] = {sb.x, sb.y, sb.z, sb.w};
+                    float v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int s = acc[i][j][4 * q + r];
+                        if (GATED)
+                            v[r] = silu_mul(i8_rescale(s, s_x[j], g4[r]),
+                                            i8_rescale(acc[GATED ? i + NI / 2 : i][j][4 * q + r], s_x[j], u4[r]));
+                        else
+                            v[r] = biased ? i8_rescale(s, s_x[j], g4[r], b4[r]) : i8_rescale(s, s_x[j], g4[r]);
+                    }
+                    if (YT == Q8_T_F32)
+                        *(float4 *)(turn + li * 128 + 16 * ((2 * q + h) ^ ((li >> 1) & 7))) =
+                            make_float4(v[0], v[1], v[2], v[3]);
+                    else
+                        *(u32x2 *)(turn + li * 128 + 16 * ((4 * ip + q) ^ ((li >> 1) & 7)) + 8 * h) =
+                            (u32x2){pack2<YT>(v[0], v[1]), pack2<YT>(v[2], v[3])};
+                }
+            wave_lds_sync();
+#pragma unroll
+            for (int e = 0; e < kChunks / 2; ++e) {
+                const int row = e * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
+                const u32x4 o = *(const u32x4 *)(turn + row * 128 + 16 * (c ^ ((row >> 1) & 7)));
+                const int64_t t = m0 + (wm * MI + j) * 32 + row;
+                const int64_t n = n0 + wn * kWaveCols + 32 * i0 + c * (16 / kES);
+                if (t < a.m && n < a.n) store16<YT>(a.y, t * a.y_stride + n, o, (int)min((int64_t)8, a.n - n));
             }
+            wave_lds_sync();
+        }
     }
 }
 
