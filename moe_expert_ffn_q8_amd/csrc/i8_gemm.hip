@@ -12,15 +12,20 @@
 //    computes NI x MI tiles of 32 x 32.  In the gated form half of a wave's
 //    weight rows are gate rows and the other half the up rows of the same
 //    outputs, so that silu(g) * u is formed in registers.
-//  * k is walked in steps of 64 bytes.  A step of both operands goes straight
+//  * k is walked in steps of 128 bytes.  A step of both operands goes straight
 //    from HBM to LDS (16-byte buffer loads in LDS DMA mode; rows past m or n
-//    and bytes past k read as zero) into a ring of kStages stages: the loads of
-//    step s + kStages go out when the last fragments of step s are in
-//    registers, and kStages - 1 steps pass before they are waited for.
-//  * A staged row is 64 bytes, its 16-byte chunk c at slot c ^ ((row/4) % 4):
+//    and bytes past k read as zero): three stages for the weights, which come
+//    from HBM, two for the tokens, which the XCD's L2 holds, 160 KB at
+//    256 x 256.  A stage is refilled as soon as its last fragments are in
+//    registers.  (Steps of 64 bytes allow five stages, but such half-line rows
+//    reach LDS at 58 GB/s per CU against 123: 264 us for the gated
+//    2048 x 4096 x 2*14336.)
+//  * A staged row is 128 bytes, its 16-byte chunk c at slot c ^ ((row/2) % 8):
 //    the 16-byte fragment reads of 16 consecutive rows then fall on all 64
 //    banks once, and the swizzle costs nothing (the DMA's LDS side is linear,
 //    the lanes' global addresses carry it).
+//  * The fragments of the next 32 bytes of k are read between the matrix
+//    instructions of these, one read after each.
 //  * Matrix operands: A = weight rows, B = tokens, so that a lane's results
 //    are runs of 4 consecutive outputs of one token.
 //  * Workgroups are dealt to the 8 XCDs round robin; each XCD takes a
@@ -36,8 +41,7 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 
-constexpr int kStep = 64;         // bytes of k per step
-constexpr int kStages = 5;        // 160 KB of LDS at 256 x 256
+constexpr int kStep = 128;        // bytes of k per step
 constexpr int kGroupM = 8;        // token tiles next to each other
 constexpr int kOut = 0x7ff00000;  // an offset past every resource: reads zero
 
@@ -50,18 +54,18 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
 {
     constexpr int kWaves = WN * WM;
     constexpr int NI = TN / WN / 32, MI = TM / WM / 32;
-    constexpr int kLoadsW = TN / 16 / kWaves, kLoadsX = TM / 16 / kWaves;
+    constexpr int kLoadsW = TN / 8 / kWaves, kLoadsX = TM / 8 / kWaves;
     constexpr int kCols = GATED ? TN / 2 : TN;          // outputs per tile
     constexpr int kWaveCols = kCols / WN;
-    static_assert(TN % (16 * kWaves) == 0 && TM % (16 * kWaves) == 0, "whole loads per wave");
+    static_assert(TN % (8 * kWaves) == 0 && TM % (8 * kWaves) == 0, "whole loads per wave");
+    static_assert(kWaves % 2 == 0, "the chunk of a lane is the same for every load");
     static_assert(!GATED || NI % 2 == 0, "gate and up halves");
     // separate objects: a fragment read then waits for its own stage's loads
-    __shared__ __align__(16) uint8_t stage0[(TN + TM) * kStep];
-    __shared__ __align__(16) uint8_t stage1[(TN + TM) * kStep];
-    __shared__ __align__(16) uint8_t stage2[(TN + TM) * kStep];
-    __shared__ __align__(16) uint8_t stage3[(TN + TM) * kStep];
-    __shared__ __align__(16) uint8_t stage4[(TN + TM) * kStep];
-    static_assert(kStages == 5, "stage0 .. stage4");
+    __shared__ __align__(16) uint8_t w0[TN * kStep];
+    __shared__ __align__(16) uint8_t w1[TN * kStep];
+    __shared__ __align__(16) uint8_t w2[TN * kStep];
+    __shared__ __align__(16) uint8_t x0[TM * kStep];
+    __shared__ __align__(16) uint8_t x1[TM * kStep];
 
     const int wave = wave_uniform((int)(threadIdx.x >> 6));
     const int lane = threadIdx.x & 63;
@@ -86,12 +90,12 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
         (void *)(a.x + m0 * a.x_stride), 0, (x_rows - 1) * x_stride + k, kBufferWord3);
     const int8_t *w_base[kLoadsW];     // (no array of resources: the host pass has no such type)
     int voff[kLoadsW + kLoadsX];
-    // load u of a wave: staged rows 16f .. 16f+15, f = wave + kWaves * u
-    const int lr = lane >> 2;
-    const int chunk = (lane & 3) ^ (lane >> 4);
+    // load u of a wave: staged rows 8f .. 8f+7, f = wave + kWaves * u
+    const int lr = lane >> 3;
+    const int chunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);   // (8f + lr)/2 % 8
 #pragma unroll
     for (int u = 0; u < kLoadsW; ++u) {
-        const int b = 16 * (wave + kWaves * u);         // of TN; 32-row groups are uniform
+        const int b = 8 * (wave + kWaves * u);          // of TN; 32-row groups are uniform
         int row = b;
         const int8_t *base = a.w + n0 * a.w_stride;
         if (GATED) {
@@ -104,24 +108,30 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
     }
 #pragma unroll
     for (int u = 0; u < kLoadsX; ++u) {
-        const int row = 16 * (wave + kWaves * u) + lr;
+        const int row = 8 * (wave + kWaves * u) + lr;
         voff[kLoadsW + u] = row < x_rows ? row * x_stride + 16 * chunk : kOut;
     }
 
-    auto issue = [&](int st, uint8_t *s) {
+    auto issue_w = [&](int st, uint8_t *s) {
         const bool in_k = 16 * chunk < k - st * kStep;
         const int so = min(st * kStep, k);       // (kOut + so stays below 2^31)
 #pragma unroll
-        for (int u = 0; u < kLoadsW + kLoadsX; ++u) {
+        for (int u = 0; u < kLoadsW; ++u) {
+            const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+                (void *)w_base[u], 0, (w_rows - 1) * w_stride + k, kBufferWord3);
+            auto *dst = (__attribute__((address_space(3))) void *)(s + 1024 * (wave + kWaves * u));
             const int off = in_k ? voff[u] : kOut;
-            const int f = u < kLoadsW ? wave + kWaves * u : TN / 16 + wave + kWaves * (u - kLoadsW);
-            auto *dst = (__attribute__((address_space(3))) void *)(s + 1024 * f);
-            if (u < kLoadsW) {
-                const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
-                    (void *)w_base[u], 0, (w_rows - 1) * w_stride + k, kBufferWord3);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, dst, 16, off, so, 0, 0);
-            } else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, dst, 16, off, so, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, dst, 16, off, so, 0, 0);
+        }
+    };
+    auto issue_x = [&](int st, uint8_t *s) {
+        const bool in_k = 16 * chunk < k - st * kStep;
+        const int so = min(st * kStep, k);       // (kOut + so stays below 2^31)
+#pragma unroll
+        for (int u = 0; u < kLoadsX; ++u) {
+            auto *dst = (__attribute__((address_space(3))) void *)(s + 1024 * (wave + kWaves * u));
+            const int off = in_k ? voff[kLoadsW + u] : kOut;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, dst, 16, off, so, 0, 0);
         }
     };
 
@@ -154,15 +164,15 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
     struct Frag {
         v4i w[NI], x[MI];
     };
-    // 32 bytes of k (k-group s of the step): lane = row li, bytes 16h .. 16h+15
-    const int row_w = (wn * NI * 32 + li) * kStep, row_x = (TN + wm * MI * 32 + li) * kStep;
-    const int swz = (li >> 2) & 3;
-    auto load = [&](const uint8_t *s, int ks, Frag &f) {
+    // 32 bytes of k (group ks of the step): lane = row li, bytes 16h .. 16h+15
+    const int row_w = (wn * NI * 32 + li) * kStep, row_x = (wm * MI * 32 + li) * kStep;
+    const int swz = (li >> 1) & 7;
+    auto load = [&](const uint8_t *sw, const uint8_t *sx, int ks, Frag &f) {
         const int c = 16 * ((2 * ks + h) ^ swz);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) f.w[i] = *(const v4i *)(s + row_w + c + i * 32 * kStep);
+        for (int i = 0; i < NI; ++i) f.w[i] = *(const v4i *)(sw + row_w + c + i * 32 * kStep);
 #pragma unroll
-        for (int j = 0; j < MI; ++j) f.x[j] = *(const v4i *)(s + row_x + c + j * 32 * kStep);
+        for (int j = 0; j < MI; ++j) f.x[j] = *(const v4i *)(sx + row_x + c + j * 32 * kStep);
     };
     auto mul = [&](const Frag &f) {
 #pragma unroll
@@ -171,47 +181,71 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
             for (int j = 0; j < MI; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[i], f.x[j], acc[i][j], 0, 0, 0);
     };
-    // this wave's loads of the next stage have landed and its reads of this one
-    // are done; then every wave's (a __syncthreads would wait for the later
-    // stages' loads too)
+    // the order of the instructions since the last mark: a fragment read after
+    // each of the first matrix instructions
+    auto interleave = [&]() {
+        constexpr int kPairs = NI + MI;
+        static_assert(kPairs <= NI * MI, "a matrix instruction for each read");
+#pragma unroll
+        for (int z = 0; z < kPairs; ++z) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+        if constexpr (NI * MI > kPairs) __builtin_amdgcn_sched_group_barrier(0x008, NI * MI - kPairs, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // this wave's loads of the next stage have landed (but not the weights of the
+    // one after it) and its reads of this one are done; then every wave's (a
+    // __syncthreads would wait for all loads)
     auto next_stage = [&]() {
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kStages - 2) * (kLoadsW + kLoadsX)) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLoadsW) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
 
     const int steps = (k + kStep - 1) / kStep;
     Frag f0, f1;
-    issue(0, stage0);
-    issue(1, stage1);
-    issue(2, stage2);
-    issue(3, stage3);
-    issue(4, stage4);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 1) * (kLoadsW + kLoadsX)) : "memory");
+    issue_w(0, w0);
+    issue_x(0, x0);
+    issue_w(1, w1);
+    issue_x(1, x1);
+    issue_w(2, w2);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoadsW + kLoadsX) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    load(stage0, 0, f0);
+    load(w0, x0, 0, f0);
     // a step past the end loads zeros, so that every wait count is exact
-    auto body = [&](int st, uint8_t *cur, const uint8_t *next) {
-        load(cur, 1, f1);
+    auto body = [&](int st, uint8_t *wc, const uint8_t *wnext, uint8_t *xc, const uint8_t *xnext) {
+        load(wc, xc, 1, f1);
         mul(f0);
-        next_stage();
-        issue(st + kStages, cur);
-        load(next, 0, f0);
+        interleave();
+        load(wc, xc, 2, f0);
         mul(f1);
+        interleave();
+        load(wc, xc, 3, f1);
+        mul(f0);
+        interleave();
+        next_stage();
+        load(wnext, xnext, 0, f0);
+        issue_x(st + 2, xc);
+        issue_w(st + 3, wc);
+        mul(f1);
+        interleave();
     };
     int st = 0;
-    for (; st + kStages <= steps; st += kStages) {
-        body(st, stage0, stage1);
-        body(st + 1, stage1, stage2);
-        body(st + 2, stage2, stage3);
-        body(st + 3, stage3, stage4);
-        body(st + 4, stage4, stage0);
+    for (; st + 6 <= steps; st += 6) {
+        body(st, w0, w1, x0, x1);
+        body(st + 1, w1, w2, x1, x0);
+        body(st + 2, w2, w0, x0, x1);
+        body(st + 3, w0, w1, x1, x0);
+        body(st + 4, w1, w2, x0, x1);
+        body(st + 5, w2, w0, x1, x0);
     }
-    if (st < steps) body(st, stage0, stage1);
-    if (st + 1 < steps) body(st + 1, stage1, stage2);
-    if (st + 2 < steps) body(st + 2, stage2, stage3);
-    if (st + 3 < steps) body(st + 3, stage3, stage4);
+    if (st < steps) body(st, w0, w1, x0, x1);
+    if (st + 1 < steps) body(st + 1, w1, w2, x1, x0);
+    if (st + 2 < steps) body(st + 2, w2, w0, x0, x1);
+    if (st + 3 < steps) body(st + 3, w0, w1, x1, x0);
+    if (st + 4 < steps) body(st + 4, w1, w2, x0, x1);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (zeros still on their way to LDS)
 
     // Outputs.  Result r of a lane: weight row 8(r/4) + 4h + r%4 of its tile,
@@ -219,7 +253,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
     // results round there, 32 tokens x 128 bytes at a time (swizzled as above), so
     // that a token's outputs leave as runs of 16-byte stores.
     __syncthreads();                           // every wave is done with the stages
-    float *scales = (float *)stage1;           // [TN], then bias [TN]
+    float *scales = (float *)w2;               // [TN], then bias [TN]
     if (tid < TN) {
         scales[tid] = w_scale;
         if (!GATED) scales[TN + tid] = w_bias;
@@ -229,8 +263,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
     constexpr int kOutTiles = GATED ? NI / 2 : NI;
     constexpr int kPass = kOutTiles < 4 / kES ? kOutTiles : 4 / kES;    // tiles side by side
     constexpr int kChunks = kPass * 32 * kES / 16;                      // 16-byte pieces a row
-    uint8_t *turn = stage0 + wave * 4096;
-    static_assert(kWaves * 4096 <= (TN + TM) * kStep && TN * 8 <= (TN + TM) * kStep, "fits");
+    constexpr int kPerX = TM * kStep / 4096, kPerW = TN * kStep / 4096; // waves per stage
+    static_assert(kWaves <= 2 * kPerX + kPerW && 2 * 4 <= kStep, "fits");
+    uint8_t *turn = wave < kPerX ? x0 + wave * 4096
+                    : wave < 2 * kPerX ? x1 + (wave - kPerX) * 4096 : w0 + (wave - 2 * kPerX) * 4096;
     const bool biased = !GATED && a.bias;
 #pragma unroll
     for (int j = 0; j < MI; ++j) {
