@@ -31,6 +31,8 @@
 //  * Workgroups are dealt to the 8 XCDs round robin; each XCD takes a
 //    contiguous run of tiles, up to 8 token tiles of one weight tile next to
 //    each other, so that an XCD's L2 serves both operands' reuse.
+//  * Large tiles where they fill the device, 128 x 128 ones elsewhere (rule and
+//    figures: launch_form).
 #include "i8_device.h"
 #include "q8_i8.h"
 
@@ -45,12 +47,12 @@ constexpr int kStep = 128;        // bytes of k per step
 constexpr int kGroupM = 8;        // token tiles next to each other
 constexpr int kOut = 0x7ff00000;  // an offset past every resource: reads zero
 
-struct TileGrid {
-    int tiles_n, tiles_m;
-};
-
+// One tile: outputs n0 .. (TN of them, TN/2 gated), tokens m0 .. m0 + TM - 1.
+// w0 .. x1: the stages, separate LDS objects, so that a fragment read waits for
+// its own stage's loads only.
 template <int TN, int TM, int WN, int WM, int YT, bool GATED>
-__global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a, const TileGrid g)
+__device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0, uint8_t *w0,
+                                        uint8_t *w1, uint8_t *w2, uint8_t *x0, uint8_t *x1)
 {
     constexpr int kWaves = WN * WM;
     constexpr int NI = TN / WN / 32, MI = TM / WM / 32;
@@ -60,27 +62,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
     static_assert(TN % (8 * kWaves) == 0 && TM % (8 * kWaves) == 0, "whole loads per wave");
     static_assert(kWaves % 2 == 0, "the chunk of a lane is the same for every load");
     static_assert(!GATED || NI % 2 == 0, "gate and up halves");
-    // separate objects: a fragment read then waits for its own stage's loads
-    __shared__ __align__(16) uint8_t w0[TN * kStep];
-    __shared__ __align__(16) uint8_t w1[TN * kStep];
-    __shared__ __align__(16) uint8_t w2[TN * kStep];
-    __shared__ __align__(16) uint8_t x0[TM * kStep];
-    __shared__ __align__(16) uint8_t x1[TM * kStep];
 
     const int wave = wave_uniform((int)(threadIdx.x >> 6));
     const int lane = threadIdx.x & 63;
     const int wn = wave / WM, wm = wave % WM;
     const int h = lane >> 5, li = lane & 31;
-
-    // this workgroup's tile
-    const int nwg = g.tiles_n * g.tiles_m;
-    const int xcd = blockIdx.x & 7, per = nwg >> 3, rest = nwg & 7;
-    const int work = xcd * per + min(xcd, rest) + (blockIdx.x >> 3);
-    const int group = work / (kGroupM * g.tiles_n);
-    const int gm = min(kGroupM, g.tiles_m - group * kGroupM);
-    const int in = work - group * kGroupM * g.tiles_n;
-    const int64_t n0 = (int64_t)(in / gm) * kCols;
-    const int64_t m0 = (int64_t)(group * kGroupM + in % gm) * TM;
 
     // operand rows of the tile
     const int k = (int)a.k;
@@ -314,24 +300,99 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void i8_gemm_kernel(const I8Args a
     }
 }
 
-template <int TN, int TM, int WN, int WM, int YT, bool GATED>
-int launch_tiles(const I8Args &a, hipStream_t stream)
+// Tiles in work order: up to kGroupM token tiles of one weight tile next to
+// each other.
+struct TileGrid {
+    int tiles_n, tiles_m;
+    int whole;                   // LARGE: tiles computed whole, the others in two halves
+
+    __device__ __forceinline__ void at(int work, int &tn, int &tm) const
+    {
+        const int group = work / (kGroupM * tiles_n);
+        const int gm = min(kGroupM, tiles_m - group * kGroupM);
+        const int in = work - group * kGroupM * tiles_n;
+        tn = in / gm;
+        tm = group * kGroupM + in % gm;
+    }
+};
+
+// Item b of n, dealt round robin to the 8 XCDs, as a run of items per XCD.
+__device__ __forceinline__ int xcd_run(int b, int n)
 {
-    const int64_t cols = GATED ? TN / 2 : TN;
-    const int64_t tn = (a.n + cols - 1) / cols, tm = (a.m + TM - 1) / TM;
-    if (tn * tm >= ((int64_t)1 << 22)) return Q8_E_UNSUPPORTED;
-    hipLaunchKernelGGL((i8_gemm_kernel<TN, TM, WN, WM, YT, GATED>), dim3((unsigned)(tn * tm)),
-                       dim3(64 * WN * WM), 0, stream, a, (TileGrid{(int)tn, (int)tm}));
-    return hipGetLastError() == hipSuccess ? 0 : -6;
+    const int xcd = b & 7, per = n >> 3, rest = n & 7;
+    return xcd * per + min(xcd, rest) + (b >> 3);
+}
+
+// 256 x 256, one workgroup of 8 waves per CU: 2.5 POPS where all CUs have work.
+// The last tiles, where they would occupy half of the CUs or fewer, are
+// computed as halves of 128 tokens, on twice as many CUs.
+template <int YT, bool GATED>
+__global__ __launch_bounds__(512, 2) void i8_large_kernel(const I8Args a, const TileGrid g)
+{
+    __shared__ __align__(16) uint8_t w0[256 * kStep];
+    __shared__ __align__(16) uint8_t w1[256 * kStep];
+    __shared__ __align__(16) uint8_t w2[256 * kStep];
+    __shared__ __align__(16) uint8_t x0[256 * kStep];
+    __shared__ __align__(16) uint8_t x1[256 * kStep];
+    constexpr int kCols = GATED ? 128 : 256;
+    const int b = blockIdx.x;
+    int tn, tm;
+    if (b < g.whole) {
+        g.at(xcd_run(b, g.whole), tn, tm);
+        i8_tile<256, 256, 4, 2, YT, GATED>(a, (int64_t)tn * kCols, (int64_t)tm * 256, w0, w1, w2, x0, x1);
+    } else {
+        const int half = xcd_run(b - g.whole, 2 * (g.tiles_n * g.tiles_m - g.whole));
+        g.at(g.whole + half / 2, tn, tm);
+        const int64_t m0 = (int64_t)tm * 256 + 128 * (half & 1);
+        if (m0 < a.m)
+            i8_tile<256, 128, 4, 2, YT, GATED>(a, (int64_t)tn * kCols, m0, w0, w1, w2, x0, x1);
+    }
+}
+
+// 128 x 128, two workgroups of 4 waves per CU.
+template <int YT, bool GATED>
+__global__ __launch_bounds__(256, 2) void i8_medium_kernel(const I8Args a, const TileGrid g)
+{
+    __shared__ __align__(16) uint8_t w0[128 * kStep];
+    __shared__ __align__(16) uint8_t w1[128 * kStep];
+    __shared__ __align__(16) uint8_t w2[128 * kStep];
+    __shared__ __align__(16) uint8_t x0[128 * kStep];
+    __shared__ __align__(16) uint8_t x1[128 * kStep];
+    int tn, tm;
+    g.at(xcd_run(blockIdx.x, g.tiles_n * g.tiles_m), tn, tm);
+    i8_tile<128, 128, 2, 2, YT, GATED>(a, (int64_t)tn * (GATED ? 64 : 128), (int64_t)tm * 128, w0, w1,
+                                       w2, x0, x1);
+}
+
+TileGrid tile_grid(const I8Args &a, bool gated, int tile)
+{
+    const int64_t cols = gated ? tile / 2 : tile;
+    const int64_t tn = (a.n + cols - 1) / cols, tm = (a.m + tile - 1) / tile;
+    if (tn * tm >= ((int64_t)1 << 22)) return {0, 0, 0};
+    return {(int)tn, (int)tm, (int)(tn * tm)};
 }
 
 template <int YT, bool GATED>
 int launch_form(const I8Args &a, hipStream_t stream)
 {
-    const int64_t cols = GATED ? 128 : 256;
-    if ((a.n + cols - 1) / cols * ((a.m + 255) / 256) >= 256)
-        return launch_tiles<256, 256, 4, 2, YT, GATED>(a, stream);
-    return launch_tiles<128, 128, 2, 2, YT, GATED>(a, stream);
+    TileGrid large = tile_grid(a, GATED, 256);
+    const TileGrid medium = tile_grid(a, GATED, 128);
+    const int tiles = large.tiles_n * large.tiles_m, mtiles = medium.tiles_n * medium.tiles_m;
+    if (!mtiles) return Q8_E_UNSUPPORTED;
+    // Rounds of the device's 256 CUs at the times of one round, in us at
+    // k = 4096: 56 for 256 tiles of 256 x 256, 36 for 256 halves, 35 for 512
+    // tiles of 128 x 128, 25 for 256 of them (the same ratios at other k).
+    const int rest = tiles % 256;
+    const int cost_large = tiles / 256 * 56 + (rest == 0 ? 0 : rest <= 128 ? 36 : 56);
+    const int cost_medium = mtiles <= 256 ? 25 : (mtiles + 511) / 512 * 35;
+    if (cost_large <= cost_medium) {
+        if (rest <= 128) large.whole -= rest;
+        hipLaunchKernelGGL((i8_large_kernel<YT, GATED>), dim3((unsigned)(2 * tiles - large.whole)),
+                           dim3(512), 0, stream, a, large);
+    } else
+        hipLaunchKernelGGL((i8_medium_kernel<YT, GATED>), dim3((unsigned)mtiles), dim3(256), 0, stream,
+                           a, medium);
+    return hipGetLastError() == hipSuccess ? 0 : -6;
 }
 
 template <int YT>
