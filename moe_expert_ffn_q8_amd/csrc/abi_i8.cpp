@@ -43,7 +43,8 @@ int i8_product(const void *x, int x_type, int64_t x_row_stride, const float *x_s
     if (int rc = check_i8_k(k)) return rc;
     if (n < 0 || m < 0) return Q8_E_SHAPE;
     if (!float_type(y_type) || (x_type != Q8_T_I8 && !float_type(x_type))) return Q8_E_UNSUPPORTED;
-    if (n > q8::kI8MaxRows || m > q8::kI8MaxRows) return Q8_E_UNSUPPORTED;
+    if (n > q8::kI8MaxRows || m > q8::kI8MaxRows || (m > 0 && n > q8::kI8MaxOutputs / m))
+        return Q8_E_UNSUPPORTED;
     if (n == 0 || m == 0) return Q8_OK;
     const bool codes = x_type == Q8_T_I8;
     if (!x || !w || !w_scale || !y || (codes && !x_scale)) return Q8_E_NULL;
@@ -74,7 +75,7 @@ int i8_product(const void *x, int x_type, int64_t x_row_stride, const float *x_s
             return hip_status(rc);
         a.x = q; a.x_scale = s; a.x_stride = up16(k);
     }
-    return hip_status(m <= q8::kI8StreamMaxM
+    return hip_status(q8::i8_stream_ok(a, gated)
                           ? q8::launch_i8_stream(a, nullptr, Q8_T_I8, 0, gated, st)
                           : q8::launch_i8_gemm(a, gated, st));
 }

@@ -1,6 +1,7 @@
 // i8_stream.hip -- the 8-bit products with token and channel scales for few
-// token rows (decode, small batches): the weights are streamed once and HBM
-// bounds the kernel.
+// token rows (decode, small batches), where HBM bounds the kernel, and for
+// small matrices, where the length of k does: no workgroup waits for another
+// and its four waves walk four parts of k.
 //
 // Work decomposition:
 //  * Workgroup = 4 waves, 16*NI weight rows x 16*MT tokens, all of k: the
@@ -135,7 +136,7 @@ struct Rows<-1> {
 // NI: 16-row weight tiles (in the gated form NI/2 of gate rows, then NI/2 of
 // the up rows of the same outputs).  MT: 16-token tiles.
 // XT: the type of token rows taken as given (XL), or -1.
-template <int NI, int MT, int D, int XT, bool GATED>
+template <int NI, int MT, int XT, bool GATED>
 __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs p)
 {
     constexpr bool XL = XT >= 0;
@@ -144,11 +145,9 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
     constexpr int kStage = kRows * kStep;
     constexpr int kLoads = kRows / 8;                    // DMA instructions per stage
     constexpr int kOuts = 16 * (GATED ? NI / 2 : NI);    // outputs per tile
-    static_assert(D == 2 || D == 3, "ring depth");
     static_assert(!XL || MT == 1, "few rows");
     __shared__ __align__(16) uint8_t ring0[kWaves][kStage];
     __shared__ __align__(16) uint8_t ring1[kWaves][kStage];
-    __shared__ __align__(16) uint8_t ring2[D > 2 ? kWaves : 1][D > 2 ? kStage : 16];
     __shared__ __align__(16) uint8_t xs[XL ? kXlValues : 16];
     __shared__ float xl_scale[kXlRows];
     __shared__ uint32_t xl_amax[kWaves][kXlRows];
@@ -207,9 +206,8 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
     const int its = (k + kStep * kWaves - 1) / (kStep * kWaves);
     const int swz = (li >> 1) & 7;
     auto body = [&](int it, uint8_t *s) {
-        // D - 1 later stages may still be in flight
-        if (D == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
-        if (D == 3) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+        // the next stage may still be in flight
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
         const int st = it * kWaves + wave;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
@@ -233,7 +231,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], b[j], acc[i][j], 0, 0, 0);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the stage is read
-        issue(it + D, s);
+        issue(it + 2, s);
     };
 
     // the scales this lane needs at the end: tiles wave, wave + 4, ...
@@ -260,16 +258,14 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
     rows.load(p, per);
     issue(0, ring0[wave]);
     issue(1, ring1[wave]);
-    if (D > 2) issue(2, ring2[wave]);
     if (XL) {
         rows.store(p, per, xs, xl_scale, xl_amax);
         lds_barrier();
     }
     // whole turns of the ring: stages past the end hold zeros
-    for (int it = 0; it < its; it += D) {
+    for (int it = 0; it < its; it += 2) {
         body(it, ring0[wave]);
         body(it + 1, ring1[wave]);
-        if (D > 2) body(it + 2, ring2[wave]);
     }
 
     // join the waves' sums: each wave its own ring slot, then wave w finishes
@@ -318,29 +314,50 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
     }
 }
 
-template <int NI, int MT, int D, int XT>
+int64_t workgroups(const I8Args &a, bool gated, int ni, int mt)
+{
+    const int64_t outs = 16 * (gated ? ni / 2 : ni);
+    return (a.n + outs - 1) / outs * ((a.m + 16 * mt - 1) / (16 * mt));
+}
+
+template <int NI, int MT, int XT>
 int launch(const StreamArgs &p, bool gated, hipStream_t stream)
 {
-    const int64_t outs = 16 * (gated ? NI / 2 : NI);
-    const int64_t tiles = (p.a.n + outs - 1) / outs;
-    if (tiles >= (1 << 24)) return Q8_E_UNSUPPORTED;
-    const dim3 grid((unsigned)tiles, (unsigned)((p.a.m + 16 * MT - 1) / (16 * MT)));
+    const int64_t by = (p.a.m + 16 * MT - 1) / (16 * MT), bx = workgroups(p.a, gated, NI, MT) / by;
+    if (bx >= (1 << 24)) return Q8_E_UNSUPPORTED;
+    const dim3 grid((unsigned)bx, (unsigned)by);
     if (gated)
-        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, D, XT, true>), grid, dim3(64 * kWaves), 0, stream, p);
+        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, XT, true>), grid, dim3(64 * kWaves), 0, stream, p);
     else
-        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, D, XT, false>), grid, dim3(64 * kWaves), 0, stream, p);
+        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, XT, false>), grid, dim3(64 * kWaves), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -6;
 }
 
-// 64-row workgroups where they fill the device, else 32-row ones
-template <int XT>
-int launch_16(const StreamArgs &p, bool gated, hipStream_t stream)
+// The smallest workgroups of which the device needs at most one per CU are the
+// fastest (a workgroup's time grows with its rows: at k = 4096 7.6 us for 32
+// weight rows x 16 tokens, 8.4 for 32 x 32, 10.6 for 32 x 64, 14.1 for
+// 64 x 64); 0 where even 64 x 64 ones are more.
+struct Shape {
+    int ni, mt;
+};
+
+Shape shape(const I8Args &a, bool gated)
 {
-    const bool wide = (gated ? 2 * p.a.n : p.a.n) >= 64 * 512;
-    return wide ? launch<4, 1, 2, XT>(p, gated, stream) : launch<2, 1, 3, XT>(p, gated, stream);
+    const Shape s[4] = {{2, 1}, {2, 2}, {2, 4}, {4, 4}};
+    for (int i = 0; i < 4; ++i)
+        if ((i == 0 || 8 * s[i].mt < a.m) && workgroups(a, gated, s[i].ni, s[i].mt) <= 256) return s[i];
+    return {0, 0};
+}
+
+template <int XT>
+int launch_rows(const StreamArgs &p, bool gated, hipStream_t stream)
+{
+    return shape(p.a, gated).ni ? launch<2, 1, XT>(p, gated, stream) : launch<4, 1, XT>(p, gated, stream);
 }
 
 }  // namespace
+
+bool i8_stream_ok(const I8Args &a, bool gated) { return a.m <= 64 || shape(a, gated).ni != 0; }
 
 bool i8_inline_ok(int64_t m, int64_t k) { return m <= kXlRows && m * k <= kXlValues; }
 
@@ -350,13 +367,18 @@ int launch_i8_stream(const I8Args &a, const void *xf, int xf_type, int64_t xf_st
     StreamArgs p;
     p.a = a;
     p.xf = xf; p.xf_stride = xf_stride;
-    if (xf && xf_type == Q8_T_F32) return launch_16<Q8_T_F32>(p, gated, stream);
-    if (xf && xf_type == Q8_T_F16) return launch_16<Q8_T_F16>(p, gated, stream);
-    if (xf && xf_type == Q8_T_BF16) return launch_16<Q8_T_BF16>(p, gated, stream);
-    if (xf) return launch_16<Q8_T_I8>(p, gated, stream);
-    if (a.m <= 16) return launch_16<-1>(p, gated, stream);
-    if (a.m <= 32) return launch<4, 2, 2, -1>(p, gated, stream);
-    return launch<4, 4, 2, -1>(p, gated, stream);
+    if (xf && xf_type == Q8_T_F32) return launch_rows<Q8_T_F32>(p, gated, stream);
+    if (xf && xf_type == Q8_T_F16) return launch_rows<Q8_T_F16>(p, gated, stream);
+    if (xf && xf_type == Q8_T_BF16) return launch_rows<Q8_T_BF16>(p, gated, stream);
+    if (xf) return launch_rows<Q8_T_I8>(p, gated, stream);
+    const Shape s = shape(a, gated);
+    if (s.mt == 1) return launch<2, 1, -1>(p, gated, stream);
+    if (s.mt == 2) return launch<2, 2, -1>(p, gated, stream);
+    if (s.ni == 2) return launch<2, 4, -1>(p, gated, stream);
+    // HBM bounds it: 64 weight rows, all tokens at once where they are 64 or fewer
+    if (a.m <= 16) return launch<4, 1, -1>(p, gated, stream);
+    if (a.m <= 32) return launch<4, 2, -1>(p, gated, stream);
+    return launch<4, 4, -1>(p, gated, stream);
 }
 
 }  // namespace q8

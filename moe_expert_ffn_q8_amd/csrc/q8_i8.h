@@ -12,6 +12,7 @@ constexpr int64_t kI8MaxK = 131040;
 // Tile rows are addressed with 32-bit byte offsets: 256 rows of at most 4 MiB.
 constexpr int64_t kI8MaxRowBytes = (int64_t)1 << 22;
 constexpr int64_t kI8MaxRows = (int64_t)1 << 27;
+constexpr int64_t kI8MaxOutputs = (int64_t)1 << 36;
 
 // One product, already validated.  x: codes with x_scale per row.
 struct I8Args {
@@ -31,10 +32,10 @@ struct I8Args {
 int launch_i8_quantize(const void *x, int type, int64_t x_stride, int8_t *q, int64_t q_stride,
                        float *scale, int64_t n_rows, int64_t k, hipStream_t stream);
 
-// Few token rows (m <= kI8StreamMaxM), weights streamed once.  With xf the
-// token rows are taken as given (xf_type, Q8_T_I8 included; bytes per row
-// xf_stride) where i8_inline_ok, and a.x is not read.
-constexpr int64_t kI8StreamMaxM = 64;
+// Few token rows or few outputs (i8_stream_ok), weights streamed once for at
+// most 64 rows.  With xf the token rows are taken as given (xf_type, Q8_T_I8
+// included; bytes per row xf_stride) where i8_inline_ok, and a.x is not read.
+bool i8_stream_ok(const I8Args &a, bool gated);
 bool i8_inline_ok(int64_t m, int64_t k);
 int launch_i8_stream(const I8Args &a, const void *xf, int xf_type, int64_t xf_stride, bool gated,
                      hipStream_t stream);
