@@ -9,11 +9,11 @@
 //
 // The largest n_top logits: every wave keeps candidates of its own, (value,
 // lowest index first) as one 64-bit key, in LDS, and the key that a logit has to
-// pass.  After turns 1, 2, 4, 8, ... the workgroup sets a common bound: with r =
-// n_top / waves, the (n_top / r)-th largest of the waves' r-th largest lane
-// maxima so far (n_top logits reach it), so few logits ever get in.  When a
-// wave's 128 places are full, each candidate counts the larger ones (its rank)
-// and the first n_top stay.  Most 16-byte groups are dismissed by their maximum, which
+// pass.  After turns 1, 2, 4, 8, ... the workgroup sets a common bound: the
+// n_top-th largest of its 256 lanes' (or quads of lanes') maxima so far, which
+// n_top logits reach and few more, so few logits ever get in.  When a wave's
+// 128 places are full, each candidate counts the larger ones (its rank) and the
+// first n_top stay.  Most 16-byte groups are dismissed by their maximum, which
 // the sums need anyway.
 #include "i8_device.h"
 #include "q8_i8.h"
@@ -113,16 +113,43 @@ __device__ __forceinline__ float key_value(uint64_t key)
 
 __device__ __forceinline__ int key_index(uint64_t key) { return (int)~(uint32_t)key; }
 
-// The n-th largest of one key per lane, its low half cut (0: fewer than n
-// lanes have one).
-__device__ __forceinline__ uint32_t nth_key(uint32_t key, int n)
+// Moves within rows of 16 lanes.
+template <int Ctrl>
+__device__ __forceinline__ uint32_t row_move(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, Ctrl, 0xf, 0xf, false);
+}
+
+// The n-th largest of 256 keys, four per lane, its low half cut (0: fewer than
+// n keys are not 0).
+__device__ __forceinline__ uint32_t nth_key(u32x4 key, int n)
 {
     uint32_t t = 0;
     for (int b = 31; b >= 16; --b) {
         const uint32_t c = t | (1u << b);
-        if (__popcll(__ballot(key >= c)) >= n) t = c;
+        if (__popcll(__ballot(key.x >= c)) + __popcll(__ballot(key.y >= c)) +
+                __popcll(__ballot(key.z >= c)) + __popcll(__ballot(key.w >= c)) >= n)
+            t = c;
     }
     return t;
+}
+
+// f(rank, key) for the first n of `count` different keys in LDS (0: none), by
+// a whole workgroup: eight lanes count the larger ones of each.
+template <class F>
+__device__ __forceinline__ void by_rank(const uint64_t *keys, int count, int n, int threads, F f)
+{
+    const int sub = threadIdx.x & 7;
+    for (int c0 = 0; c0 < count; c0 += threads / 8) {
+        const int c = c0 + (threadIdx.x >> 3);
+        const uint64_t k = c < count ? keys[c] : 0;
+        int rank = 0;
+        for (int j = sub; j < count; j += 8) rank += keys[j] > k;
+        rank += (int)row_move<0xb1>((uint32_t)rank);     // quad_perm:[1,0,3,2]
+        rank += (int)row_move<0x4e>((uint32_t)rank);     // quad_perm:[2,3,0,1]
+        rank += (int)row_move<0x141>((uint32_t)rank);    // row_half_mirror
+        if (sub == 0 && k != 0 && rank < n) f(rank, k);
+    }
 }
 
 // One wave's candidates.  thr: what a key has to exceed; least: a value below
@@ -148,16 +175,18 @@ struct Top {
     // Ranks; the first n stay, in order.
     __device__ __forceinline__ void compact(int lane)
     {
-        if (lane == 0 && count < kPlaces) place[count] = 0;       // the pair read past the end
+        if (lane < 8 && count + lane < kPlaces) place[count + lane] = 0;     // read by eights
         wave_lds_sync();
         const uint64_t k0 = lane < count ? place[lane] : 0;
         const uint64_t k1 = 64 + lane < count ? place[64 + lane] : 0;
         int r0 = 0, r1 = 0;
-        for (int i = 0; i < count; i += 2) {
-            const ulonglong2 o = *(const ulonglong2 *)(place + i);
-            r0 += (o.x > k0) + (o.y > k0);
-            r1 += (o.x > k1) + (o.y > k1);
-        }
+        for (int i = 0; i < count; i += 8)
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const ulonglong2 o = *(const ulonglong2 *)(place + i + j);
+                r0 += (o.x > k0) + (o.y > k0);
+                r1 += (o.x > k1) + (o.y > k1);
+            }
         wave_lds_sync();
         if (lane < count && r0 < n) place[r0] = k0;
         if (64 + lane < count && r1 < n) place[r1] = k1;
@@ -317,11 +346,28 @@ __device__ Stat slow_stat(const LogprobArgs &a, int64_t row, Stat *part, int wav
     return st;
 }
 
+// The given token that a thread writes, read before it is needed.
+struct Given {
+    int token;
+    float x;
+};
+
+template <int T>
+__device__ __forceinline__ Given given(const LogprobArgs &a, int64_t row, int i)
+{
+    Given g = {-1, 0.0f};
+    if (i < a.n_given) {
+        g.token = a.tokens[row * a.n_given + i];
+        if (g.token >= 0 && g.token < a.n_vocab) g.x = logit<T>(a, row, g.token);
+    }
+    return g;
+}
+
 // Outputs of a row from its (r, S, W), the same in every thread; `tops` are
-// `count` candidates in LDS, n_top of them the answer.
+// `count` candidates in LDS, n_top of them the answer; g: token threadIdx.x.
 template <int T>
 __device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stat st, Stat *part,
-                                       int waves, const uint64_t *tops, int count)
+                                       int waves, const uint64_t *tops, int count, Given g)
 {
     const int tid = threadIdx.x, threads = 64 * waves;
     float shift = 0.0f;                          // r L as rounded, minus r L
@@ -338,23 +384,14 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stat s
     }
     auto lp = [&](float x) { return empty ? lse : x - lse; };
     for (int i = tid; i < a.n_given; i += threads) {
-        const int64_t at = row * a.n_given + i;
-        const int tok = a.tokens[at];
-        a.logprob[at] = tok >= 0 && tok < a.n_vocab ? lp(logit<T>(a, row, tok)) : __builtin_nanf("");
+        if (i != tid) g = given<T>(a, row, i);
+        a.logprob[row * a.n_given + i] =
+            g.token >= 0 && g.token < a.n_vocab ? lp(g.x) : __builtin_nanf("");
     }
-    for (int i = tid; i < count; i += threads) {
-        const uint64_t k = tops[i];
-        if (k == 0) continue;
-        int rank = 0;
-        for (int j = 0; j < count; j += 2) {
-            const ulonglong2 o = *(const ulonglong2 *)(tops + j);
-            rank += (o.x > k) + (o.y > k);
-        }
-        if (rank < a.n_top) {
-            a.top_ids[row * a.n_top + rank] = key_index(k);
-            a.top_logprobs[row * a.n_top + rank] = lp(key_value(k));
-        }
-    }
+    by_rank(tops, count, a.n_top, threads, [&](int rank, uint64_t k) {
+        a.top_ids[row * a.n_top + rank] = key_index(k);
+        a.top_logprobs[row * a.n_top + rank] = lp(key_value(k));
+    });
 }
 
 template <int T, int W, bool TOP>
@@ -362,12 +399,13 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
 {
     typedef typename Elem<T>::type E;
     constexpr int V = kVec<T>;
+    static_assert(W == 4 || W == 16, "256 lanes, or quads of them");
     __shared__ Stat part[W];
     __shared__ __align__(16) uint64_t places[TOP ? W : 1][TOP ? kPlaces : 2];
-    __shared__ __align__(16) uint64_t merged[TOP ? W * kLogprobMaxTop + 2 : 2];
+    __shared__ __align__(16) uint64_t merged[TOP ? W * kLogprobMaxTop : 2];
     __shared__ __align__(16) u32x4 pend_v[TOP ? W : 1][TOP ? kPend : 1];
     __shared__ int pend_i[TOP ? W : 1][TOP ? kPend : 1];
-    __shared__ uint32_t bounds[2][W];
+    __shared__ __align__(16) uint32_t bounds[2][256];
     __shared__ int counts[W];
     const int64_t row = blockIdx.y;
     const int lane = threadIdx.x & 63, wave = wave_uniform((int)(threadIdx.x >> 6));
@@ -401,6 +439,8 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
     const int edge_i = lane < head ? lane : lane + vecs * V;
     const float edge = lane < head + tail && wave == W - 1 ? (float)x0[edge_i] : -INFINITY;
     if (vecs > 0) fetch(wave * turn);
+    Given g = {-1, 0.0f};
+    if (wk.parts == 1) g = given<T>(a, row, threadIdx.x);
     float lane_max = __builtin_nanf("");
     for (int it = 0; it * W * turn < vecs; ++it) {
         const int v0 = (it * W + wave) * turn;
@@ -433,15 +473,16 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
             for (int u = 0; u < kLoads; ++u)
                 lane_max = fmaxf(lane_max, v0 + 64 * u + lane < vecs ? best[u] : __builtin_nanf(""));
             if ((it & (it + 1)) == 0) {            // turns 1, 2, 4, 8, ...
-                // waves that have had a whole turn, or the first
-                const int full = max(min(vecs / turn, W), 1);
-                const int each = (a.n_top + full - 1) / full;
-                const uint32_t mine = nth_key(value_key(lane_max), each);
+                uint32_t mine = value_key(lane_max);
+                if (W == 16) {                     // 256 quads
+                    mine = max(mine, row_move<0xb1>(mine));
+                    mine = max(mine, row_move<0x4e>(mine));
+                }
                 // (a wave is at most one barrier ahead: two sets are enough)
                 uint32_t *set = bounds[__builtin_popcount(it) & 1];
-                if (lane == 0) set[wave] = mine;
+                if (W == 4 || lane % 4 == 0) set[threadIdx.x / (W / 4)] = mine;
                 __syncthreads();
-                const uint32_t all = nth_key(lane < W ? set[lane] : 0, (a.n_top + each - 1) / each);
+                const uint32_t all = nth_key(*(const u32x4 *)(set + 4 * lane), a.n_top);
                 const uint64_t t = ((uint64_t)all << 32) - 1;
                 if (all && t > top.thr) top.set(t);
             }
@@ -471,7 +512,7 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
     __syncthreads();
     int count = 0;
     if (TOP) {
-        // the waves' candidates behind each other, a 0 behind the last
+        // the waves' candidates behind each other
         int at = 0;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
@@ -479,14 +520,13 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
             count += counts[w];
         }
         for (int i = lane; i < top.count; i += 64) merged[at + i] = top.place[i];
-        if (threadIdx.x == 0) merged[count] = 0;
     }
     st = stat_zero();
     if (lane < W) st = part[lane];
     st = wave_join(st);
     __syncthreads();
     if (wk.parts == 1) {
-        finish<T>(a, row, st, part, W, merged, count);
+        finish<T>(a, row, st, part, W, merged, count, g);
         return;
     }
     const int64_t slot = row * wk.parts + blockIdx.x;
@@ -497,16 +537,7 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
         const int have = min(len, a.n_top);
         for (int i = threadIdx.x; i < a.n_top; i += 64 * W)
             if (i >= have) out[i] = 0;
-        for (int i = threadIdx.x; i < count; i += 64 * W) {
-            const uint64_t k = merged[i];
-            if (k == 0) continue;
-            int rank = 0;
-            for (int j = 0; j < count; j += 2) {
-                const ulonglong2 o = *(const ulonglong2 *)(merged + j);
-                rank += (o.x > k) + (o.y > k);
-            }
-            if (rank < a.n_top) out[rank] = k;
-        }
+        by_rank(merged, count, a.n_top, 64 * W, [&](int rank, uint64_t k) { out[rank] = k; });
     }
 }
 
@@ -515,30 +546,40 @@ template <int T>
 __global__ __launch_bounds__(256) void logprob_join_kernel(const LogprobArgs a, const Work wk)
 {
     __shared__ Stat part[4];
-    __shared__ __align__(16) uint64_t keys[kMaxParts * kLogprobMaxTop + 2];
+    __shared__ __align__(16) uint64_t keys[kMaxParts * kLogprobMaxTop];
     __shared__ int count;
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63;
+    const Given g = given<T>(a, row, tid);
     Stat st = stat_zero();
     if (lane < wk.parts) st = wk.stats[row * wk.parts + lane];
-    st = wave_join(st);
-    // a bound from the parts' r-th entries, as in the first turn of a part
     const uint64_t *tops = wk.tops + row * wk.parts * a.n_top;
+    uint64_t k[kMaxParts / 4];
+    const int total = wk.parts * a.n_top;
+    // (n_top <= 64: at most kMaxParts / 4 keys per thread)
+#pragma unroll
+    for (int i = 0; i < kMaxParts / 4; ++i) {
+        if (256 * i >= total) break;
+        k[i] = tid + 256 * i < total ? tops[tid + 256 * i] : 0;
+    }
+    // A bound: with r = n_top / parts, the (n_top / r)-th largest of the parts'
+    // r-th entries (n_top keys reach it).
+    uint32_t t = 0;
     if (a.n_top > 0) {
         const int each = (a.n_top + wk.parts - 1) / wk.parts;
-        const uint64_t last = lane < wk.parts ? tops[lane * a.n_top + each - 1] : 0;
-        const uint64_t t = (uint64_t)nth_key((uint32_t)(last >> 32), (a.n_top + each - 1) / each) << 32;
+        const uint32_t v = lane < wk.parts ? (uint32_t)(tops[lane * a.n_top + each - 1] >> 32) : 0;
+        t = nth_key((u32x4){v, 0, 0, 0}, (a.n_top + each - 1) / each);
         if (tid == 0) count = 0;
         __syncthreads();
-        for (int i = tid; i < wk.parts * a.n_top; i += 256) {
-            const uint64_t k = tops[i];
-            if (k != 0 && k >= t) keys[atomicAdd(&count, 1)] = k;
-        }
-        __syncthreads();
-        if (tid == 0) keys[count] = 0;
     }
+#pragma unroll
+    for (int i = 0; i < kMaxParts / 4; ++i) {
+        if (256 * i >= total) break;
+        if (k[i] != 0 && (uint32_t)(k[i] >> 32) >= t) keys[atomicAdd(&count, 1)] = k[i];
+    }
+    st = wave_join(st);
     __syncthreads();
-    finish<T>(a, row, st, part, 4, keys, a.n_top > 0 ? count : 0);
+    finish<T>(a, row, st, part, 4, keys, a.n_top > 0 ? count : 0, g);
 }
 
 // How a call is cut: waves per workgroup and parts per row.
