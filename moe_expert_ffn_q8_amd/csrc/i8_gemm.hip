@@ -380,11 +380,11 @@ int launch_form(const I8Args &a, hipStream_t stream)
     const int tiles = large.tiles_n * large.tiles_m, mtiles = medium.tiles_n * medium.tiles_m;
     if (!mtiles) return Q8_E_UNSUPPORTED;
     // Rounds of the device's 256 CUs at the times of one round, in us at
-    // k = 4096: 56 for 256 tiles of 256 x 256, 36 for 256 halves, 35 for 512
+    // k = 4096: 56 for 256 tiles of 256 x 256, 36 for 256 halves, 37 for 512
     // tiles of 128 x 128, 25 for 256 of them (the same ratios at other k).
     const int rest = tiles % 256;
     const int cost_large = tiles / 256 * 56 + (rest == 0 ? 0 : rest <= 128 ? 36 : 56);
-    const int cost_medium = mtiles <= 256 ? 25 : (mtiles + 511) / 512 * 35;
+    const int cost_medium = mtiles <= 256 ? 25 : (mtiles + 511) / 512 * 37;
     if (cost_large <= cost_medium) {
         if (rest <= 128) large.whole -= rest;
         hipLaunchKernelGGL((i8_large_kernel<YT, GATED>), dim3((unsigned)(2 * tiles - large.whole)),

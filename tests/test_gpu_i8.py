@@ -125,6 +125,9 @@ SHAPES = [(1, 1, 32), (1, 70, 64), (1, 768, 768), (1, 2051, 2080), (1, 129, 1433
           (96, 385, 736), (100, 130, 1504), (127, 1030, 224), (129, 257, 608), (200, 300, 320),
           (255, 129, 1312), (256, 256, 512), (257, 513, 448), (300, 1000, 4096), (513, 770, 1120),
           (1030, 1290, 256)]
+# enough outputs for the large tiles: whole rounds and halves (some of them past
+# the last token), one round that is not split
+LARGE = [(1100, 16640, 96), (1792, 8200, 64), (600, 14400, 160)]
 
 
 def _operands(m, rows, k, *key):
@@ -152,6 +155,26 @@ def test_up_gate(q, m, n_ff, k, t):
                             dtype=i8_ref.torch_type(t))
     ref, bound = i8_ref.gated(cx, sx, cw, sw)
     i8_ref.assert_close(h.double().cpu().numpy(), ref, bound, t, f"{m}x{n_ff}x{k}")
+
+
+@pytest.mark.parametrize("t", i8_ref.TYPES)
+@pytest.mark.parametrize("m,rows,k", LARGE)
+def test_large(q, m, rows, k, t):
+    """Both forms, the output inside a wider buffer with rows at odd elements."""
+    import torch
+    rng, cx, sx, cw, sw = _operands(m, rows, k, "large")
+    sx *= np.float32(30.0 / (np.sqrt(k) * 5500 * 3e-2))
+    x, s, w, ws = to_gpu(cx), to_gpu(sx), to_gpu(cw), to_gpu(sw)
+    bias = rng.normal(size=rows).astype(np.float32)
+    for fn, cols, ref, kw in ((q.i8_matmul, rows, i8_ref.product(cx, sx, cw, sw, bias), "y"),
+                              (q.i8_up_gate_swiglu, rows // 2, i8_ref.gated(cx, sx, cw, sw), "h")):
+        buf = torch.full((m + 2, cols + 7), 5.5, dtype=i8_ref.torch_type(t), device="cuda")
+        out = buf[1:m + 1, 3:3 + cols]
+        extra = {"bias": to_gpu(bias)} if fn is q.i8_matmul else {}
+        fn(x, w, ws, x_scale=s, **{kw: out}, **extra)
+        i8_ref.assert_close(out.double().cpu().numpy(), *ref, t, f"{m}x{rows}x{k}")
+        out.fill_(5.5)
+        assert bool((buf == 5.5).all())
 
 
 @pytest.mark.parametrize("m", [1, 3, 16, 40, 130, 300])
