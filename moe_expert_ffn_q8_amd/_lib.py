@@ -942,26 +942,29 @@ def _rows(t, name, types):
         raise TypeError(f"{name}: {t.dtype}, expected one of {[str(d) for d in types]}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a GPU tensor")
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(shape)}")
-    stride = t.stride()
-    if stride[1] != 1 and shape[1] > 1:
+    try:
+        rows, cols = t.shape
+        stride, step = t.stride()
+    except ValueError:
+        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}") from None
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return code, stride[0], shape[0], shape[1]
+    return code, stride, rows, cols
 
 
 def _vector(t, n, dtype, name):
-    _need(t, dtype, name)
+    """Address of a contiguous GPU tensor of n elements."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, name)
     if t.numel() != n:
         raise ValueError(f"{name}: {t.numel()} elements, expected {n}")
+    return t.data_ptr()
 
 
 def _on(device, *ts):
     """Every tensor of a call on `device`."""
     for t in ts:
         if t is not None and t.device != device:
-            _one_device(*ts)
             raise ValueError(f"tensors on several devices: {device}, {t.device}")
 
 
@@ -971,7 +974,7 @@ def _enqueue(name, fn, device, *args):
     at 2 us a call; the raw handle is read in 0.1.)"""
     index = device.index
     stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -995,11 +998,11 @@ def i8_quantize_rows(x, q=None, scale=None):
     _, qs, q_rows, q_k = _rows(q, "q", _INT8)
     if (q_rows, q_k) != (n_rows, k):
         raise ValueError(f"q: shape {(q_rows, q_k)}, expected {(n_rows, k)}")
-    _vector(scale, n_rows, torch.float32, "scale")
+    scale_p = _vector(scale, n_rows, torch.float32, "scale")
     device = x.device
     _on(device, q, scale)
     _enqueue("i8_quantize_rows", _lib.i8_quantize_rows, device, x.data_ptr(), xt, xs, q.data_ptr(),
-             qs, scale.data_ptr(), n_rows, k)
+             qs, scale_p, n_rows, k)
     return q, scale
 
 
@@ -1017,39 +1020,42 @@ def i8_workspace(m, k, device):
 
 def _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated):
     xt, xs, m, k = _rows(x, "x", _ACTS)
-    _, wst, rows, wk = _rows(w, "w", _INT8)
+    _, wst, n, wk = _rows(w, "w", _INT8)
     if wk != k:
         raise ValueError(f"w: rows of {wk} codes, x has {k}")
-    _vector(w_scale, rows, torch.float32, "w_scale")
+    w_scale_p = _vector(w_scale, n, torch.float32, "w_scale")
     device = x.device
+    x_scale_p = bias_p = ws_p = None
+    ws_bytes = 0
     if xt == 3:
         if x_scale is None:
             raise ValueError("x_scale: needed with int8 codes")
-        _vector(x_scale, m, torch.float32, "x_scale")
-        ws = None
+        x_scale_p = _vector(x_scale, m, torch.float32, "x_scale")
     else:
         if x_scale is not None:
             raise ValueError("x_scale: given with rows that are not int8 codes")
         if ws is not None:
-            _need(ws, torch.uint8, "ws")
-    n = rows
+            ws_bytes = ws.numel()
+            ws_p = _vector(ws, ws_bytes, torch.uint8, "ws")
+            _on(device, ws)
     if gated:
-        if rows % 2:
-            raise ValueError(f"w: {rows} rows, expected gate and up rows of one number")
-        n = rows // 2
+        if n % 2:
+            raise ValueError(f"w: {n} rows, expected gate and up rows of one number")
+        n //= 2
     if out is None:
         out = torch.empty((m, n), dtype=dtype, device=device)
     yt, ys, y_rows, y_cols = _rows(out, "h" if gated else "y", _FLOATS)
     if y_rows != m or y_cols != n:
         raise ValueError(f"{'h' if gated else 'y'}: shape {(y_rows, y_cols)}, expected {(m, n)}")
     if bias is not None:
-        _vector(bias, n, torch.float32, "bias")
-    _on(device, w, w_scale, x_scale, bias, out, ws)
-    _enqueue(name, fn, device, x.data_ptr(), xt, xs, None if x_scale is None else x_scale.data_ptr(),
-             w.data_ptr(), wst, w_scale.data_ptr(),
-             *(() if gated else (None if bias is None else bias.data_ptr(),)),
-             out.data_ptr(), yt, ys, n, k, m, None if ws is None else ws.data_ptr(),
-             0 if ws is None else ws.numel())
+        bias_p = _vector(bias, n, torch.float32, "bias")
+    _on(device, w, w_scale, x_scale, bias, out)
+    if gated:
+        _enqueue(name, fn, device, x.data_ptr(), xt, xs, x_scale_p, w.data_ptr(), wst, w_scale_p,
+                 out.data_ptr(), yt, ys, n, k, m, ws_p, ws_bytes)
+    else:
+        _enqueue(name, fn, device, x.data_ptr(), xt, xs, x_scale_p, w.data_ptr(), wst, w_scale_p,
+                 bias_p, out.data_ptr(), yt, ys, n, k, m, ws_p, ws_bytes)
     return out
 
 
@@ -1119,23 +1125,23 @@ def logprob_rows(logits, tokens=None, n_top=0, ws=None, out=None):
     device = logits.device
     if out is None:
         out = logprob_outputs(m, n_given, n_top, device)
-    logprob = out.logprob if n_given else None
-    ids, top = (out.top_ids, out.top_logprobs) if n_top else (None, None)
-    if (n_given and logprob is None) or (n_top and (ids is None or top is None)):
+    given_p = ids_p = top_p = ws_p = None
+    ws_bytes = 0
+    if (n_given and out.logprob is None) or (n_top and (out.top_ids is None or out.top_logprobs is None)):
         raise ValueError("out: lacks an output that this call has")
     if n_given:
-        _vector(logprob, m * n_given, torch.float32, "logprob")
-    _vector(out.lse, m, torch.float32, "lse")
-    _vector(out.entropy, m, torch.float32, "entropy")
+        given_p = _vector(out.logprob, m * n_given, torch.float32, "logprob")
+    lse_p = _vector(out.lse, m, torch.float32, "lse")
+    entropy_p = _vector(out.entropy, m, torch.float32, "entropy")
     if n_top:
-        _vector(ids, m * n_top, torch.int32, "top_ids")
-        _vector(top, m * n_top, torch.float32, "top_logprobs")
+        ids_p = _vector(out.top_ids, m * n_top, torch.int32, "top_ids")
+        top_p = _vector(out.top_logprobs, m * n_top, torch.float32, "top_logprobs")
     if ws is not None:
-        _need(ws, torch.uint8, "ws")
+        ws_bytes = ws.numel()
+        ws_p = _vector(ws, ws_bytes, torch.uint8, "ws")
     _on(device, tokens, ws, *out)
     _enqueue("logprob_rows", _lib.logprob_rows, device, logits.data_ptr(), t, stride, _ptr(tokens),
-             n_given, _ptr(logprob), out.lse.data_ptr(), out.entropy.data_ptr(), _ptr(ids), _ptr(top),
-             m, n_vocab, n_top, _ptr(ws), 0 if ws is None else ws.numel())
+             n_given, given_p, lse_p, entropy_p, ids_p, top_p, m, n_vocab, n_top, ws_p, ws_bytes)
     return out
 
 
