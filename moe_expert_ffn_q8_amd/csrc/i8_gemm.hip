@@ -33,6 +33,8 @@
 //    each other, so that an XCD's L2 serves both operands' reuse.
 //  * Large tiles where they fill the device, 128 x 128 ones elsewhere (rule and
 //    figures: launch_form).
+#include <type_traits>
+
 #include "i8_device.h"
 #include "q8_i8.h"
 
@@ -49,8 +51,8 @@ constexpr int kOut = 0x7ff00000;  // an offset past every resource: reads zero
 
 // One tile: outputs n0 .. (TN of them, TN/2 gated), tokens m0 .. m0 + TM - 1.
 // w0 .. x1: the stages, separate LDS objects, so that a fragment read waits for
-// its own stage's loads only.
-template <int TN, int TM, int WN, int WM, int YT, bool GATED>
+// its own stage's loads only.  STREAM: outputs are written past the caches.
+template <int TN, int TM, int WN, int WM, int YT, bool GATED, bool STREAM>
 __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0, uint8_t *w0,
                                         uint8_t *w1, uint8_t *w2, uint8_t *x0, uint8_t *x1)
 {
@@ -128,8 +130,9 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
     static_assert(TN <= 64 * kWaves, "a thread per weight row");
     if (tid < TN) {
         const int grp = tid / 32 % NI;
-        const int64_t col = n0 + (GATED ? tid / (32 * NI) * kWaveCols + 32 * (grp % (NI / 2 + !GATED)) + tid % 32
-                                        : tid);
+        const int64_t col = n0 + (!GATED ? tid
+                                         : tid / (32 * NI) * kWaveCols +
+                                               32 * (grp % (NI / 2 + !GATED)) + tid % 32);
         if (col < a.n) {
             w_scale = a.w_scale[GATED && grp >= NI / 2 ? a.n + col : col];
             if (!GATED && a.bias) w_bias = a.bias[col];
@@ -253,51 +256,60 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
     static_assert(kWaves <= 2 * kPerX + kPerW && 2 * 4 <= kStep, "fits");
     uint8_t *turn = wave < kPerX ? x0 + wave * 4096
                     : wave < 2 * kPerX ? x1 + (wave - kPerX) * 4096 : w0 + (wave - 2 * kPerX) * 4096;
-    const bool biased = !GATED && a.bias;
+    auto outputs = [&](auto with_bias) {
+        constexpr bool biased = decltype(with_bias)::value;
 #pragma unroll
-    for (int j = 0; j < MI; ++j) {
+        for (int j = 0; j < MI; ++j) {
 #pragma unroll
-        for (int i0 = 0; i0 < kOutTiles; i0 += kPass) {
+            for (int i0 = 0; i0 < kOutTiles; i0 += kPass) {
 #pragma unroll
-            for (int ip = 0; ip < kPass; ++ip)
+                for (int ip = 0; ip < kPass; ++ip)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int i = i0 + ip, row = (wn * NI + i) * 32 + 8 * q + 4 * h;
-                    const float4 sg = *(const float4 *)(scales + row);
-                    float4 su = sg, sb = sg;
-                    if (GATED) su = *(const float4 *)(scales + row + NI / 2 * 32);
-                    if (!GATED) sb = *(const float4 *)(scales + TN + row);
-                    const float g4[4] = {sg.x, sg.y, sg.z, sg.w}, u4[4] = {su.x, su.y, su.z, su.w},
-                                b4[4] = {sb.x, sb.y, sb.z, sb.w};
-                    float v[4];
+                    for (int q = 0; q < 4; ++q) {
+                        const int i = i0 + ip, row = (wn * NI + i) * 32 + 8 * q + 4 * h;
+                        const float4 sg = *(const float4 *)(scales + row);
+                        float4 su = sg, sb = sg;
+                        if (GATED) su = *(const float4 *)(scales + row + NI / 2 * 32);
+                        if (!GATED) sb = *(const float4 *)(scales + TN + row);
+                        const float g4[4] = {sg.x, sg.y, sg.z, sg.w}, u4[4] = {su.x, su.y, su.z, su.w},
+                                    b4[4] = {sb.x, sb.y, sb.z, sb.w};
+                        float v[4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int s = acc[i][j][4 * q + r];
-                        if (GATED)
-                            v[r] = silu_mul(i8_rescale(s, s_x[j], g4[r]),
-                                            i8_rescale(acc[GATED ? i + NI / 2 : i][j][4 * q + r], s_x[j], u4[r]));
+                        for (int r = 0; r < 4; ++r) {
+                            const int s = acc[i][j][4 * q + r];
+                            if (GATED)
+                                v[r] = silu_mul(
+                                    i8_rescale(s, s_x[j], g4[r]),
+                                    i8_rescale(acc[GATED ? i + NI / 2 : i][j][4 * q + r], s_x[j], u4[r]));
+                            else
+                                v[r] = biased ? i8_rescale(s, s_x[j], g4[r], b4[r])
+                                              : i8_rescale(s, s_x[j], g4[r]);
+                        }
+                        if (YT == Q8_T_F32)
+                            *(float4 *)(turn + li * 128 + 16 * ((2 * q + h) ^ ((li >> 1) & 7))) =
+                                make_float4(v[0], v[1], v[2], v[3]);
                         else
-                            v[r] = biased ? i8_rescale(s, s_x[j], g4[r], b4[r]) : i8_rescale(s, s_x[j], g4[r]);
+                            *(u32x2 *)(turn + li * 128 + 16 * ((4 * ip + q) ^ ((li >> 1) & 7)) + 8 * h) =
+                                (u32x2){pack2<YT>(v[0], v[1]), pack2<YT>(v[2], v[3])};
                     }
-                    if (YT == Q8_T_F32)
-                        *(float4 *)(turn + li * 128 + 16 * ((2 * q + h) ^ ((li >> 1) & 7))) =
-                            make_float4(v[0], v[1], v[2], v[3]);
-                    else
-                        *(u32x2 *)(turn + li * 128 + 16 * ((4 * ip + q) ^ ((li >> 1) & 7)) + 8 * h) =
-                            (u32x2){pack2<YT>(v[0], v[1]), pack2<YT>(v[2], v[3])};
-                }
-            wave_lds_sync();
+                wave_lds_sync();
 #pragma unroll
-            for (int e = 0; e < kChunks / 2; ++e) {
-                const int row = e * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
-                const u32x4 o = *(const u32x4 *)(turn + row * 128 + 16 * (c ^ ((row >> 1) & 7)));
-                const int64_t t = m0 + (wm * MI + j) * 32 + row;
-                const int64_t n = n0 + wn * kWaveCols + 32 * i0 + c * (16 / kES);
-                if (t < a.m && n < a.n) store16<YT>(a.y, t * a.y_stride + n, o, (int)min((int64_t)8, a.n - n));
+                for (int e = 0; e < kChunks / 2; ++e) {
+                    const int row = e * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
+                    const u32x4 o = *(const u32x4 *)(turn + row * 128 + 16 * (c ^ ((row >> 1) & 7)));
+                    const int64_t t = m0 + (wm * MI + j) * 32 + row;
+                    const int64_t n = n0 + wn * kWaveCols + 32 * i0 + c * (16 / kES);
+                    if (t < a.m && n < a.n)
+                        store16<YT, STREAM>(a.y, t * a.y_stride + n, o, (int)min((int64_t)8, a.n - n));
+                }
+                wave_lds_sync();
             }
-            wave_lds_sync();
         }
-    }
+    };
+    if (!GATED && a.bias)
+        outputs(std::integral_constant<bool, !GATED>());
+    else
+        outputs(std::integral_constant<bool, false>());
 }
 
 // Tiles in work order: up to kGroupM token tiles of one weight tile next to
@@ -326,7 +338,7 @@ __device__ __forceinline__ int xcd_run(int b, int n)
 // 256 x 256, one workgroup of 8 waves per CU: 2.5 POPS where all CUs have work.
 // The last tiles, where they would occupy half of the CUs or fewer, are
 // computed as halves of 128 tokens, on twice as many CUs.
-template <int YT, bool GATED>
+template <int YT, bool GATED, bool STREAM>
 __global__ __launch_bounds__(512, 2) void i8_large_kernel(const I8Args a, const TileGrid g)
 {
     __shared__ __align__(16) uint8_t w0[256 * kStep];
@@ -339,18 +351,19 @@ __global__ __launch_bounds__(512, 2) void i8_large_kernel(const I8Args a, const 
     int tn, tm;
     if (b < g.whole) {
         g.at(xcd_run(b, g.whole), tn, tm);
-        i8_tile<256, 256, 4, 2, YT, GATED>(a, (int64_t)tn * kCols, (int64_t)tm * 256, w0, w1, w2, x0, x1);
+        i8_tile<256, 256, 4, 2, YT, GATED, STREAM>(a, (int64_t)tn * kCols, (int64_t)tm * 256, w0, w1,
+                                                   w2, x0, x1);
     } else {
         const int half = xcd_run(b - g.whole, 2 * (g.tiles_n * g.tiles_m - g.whole));
         g.at(g.whole + half / 2, tn, tm);
         const int64_t m0 = (int64_t)tm * 256 + 128 * (half & 1);
         if (m0 < a.m)
-            i8_tile<256, 128, 4, 2, YT, GATED>(a, (int64_t)tn * kCols, m0, w0, w1, w2, x0, x1);
+            i8_tile<256, 128, 4, 2, YT, GATED, STREAM>(a, (int64_t)tn * kCols, m0, w0, w1, w2, x0, x1);
     }
 }
 
 // 128 x 128, two workgroups of 4 waves per CU.
-template <int YT, bool GATED>
+template <int YT, bool GATED, bool STREAM>
 __global__ __launch_bounds__(256, 2) void i8_medium_kernel(const I8Args a, const TileGrid g)
 {
     __shared__ __align__(16) uint8_t w0[128 * kStep];
@@ -360,8 +373,8 @@ __global__ __launch_bounds__(256, 2) void i8_medium_kernel(const I8Args a, const
     __shared__ __align__(16) uint8_t x1[128 * kStep];
     int tn, tm;
     g.at(xcd_run(blockIdx.x, g.tiles_n * g.tiles_m), tn, tm);
-    i8_tile<128, 128, 2, 2, YT, GATED>(a, (int64_t)tn * (GATED ? 64 : 128), (int64_t)tm * 128, w0, w1,
-                                       w2, x0, x1);
+    i8_tile<128, 128, 2, 2, YT, GATED, STREAM>(a, (int64_t)tn * (GATED ? 64 : 128), (int64_t)tm * 128,
+                                               w0, w1, w2, x0, x1);
 }
 
 TileGrid tile_grid(const I8Args &a, bool gated, int tile)
@@ -372,7 +385,7 @@ TileGrid tile_grid(const I8Args &a, bool gated, int tile)
     return {(int)tn, (int)tm, (int)(tn * tm)};
 }
 
-template <int YT, bool GATED>
+template <int YT, bool GATED, bool STREAM>
 int launch_form(const I8Args &a, hipStream_t stream)
 {
     TileGrid large = tile_grid(a, GATED, 256);
@@ -387,18 +400,26 @@ int launch_form(const I8Args &a, hipStream_t stream)
     const int cost_medium = mtiles <= 256 ? 25 : (mtiles + 511) / 512 * 37;
     if (cost_large <= cost_medium) {
         if (rest <= 128) large.whole -= rest;
-        hipLaunchKernelGGL((i8_large_kernel<YT, GATED>), dim3((unsigned)(2 * tiles - large.whole)),
+        hipLaunchKernelGGL((i8_large_kernel<YT, GATED, STREAM>), dim3((unsigned)(2 * tiles - large.whole)),
                            dim3(512), 0, stream, a, large);
     } else
-        hipLaunchKernelGGL((i8_medium_kernel<YT, GATED>), dim3((unsigned)mtiles), dim3(256), 0, stream,
+        hipLaunchKernelGGL((i8_medium_kernel<YT, GATED, STREAM>), dim3((unsigned)mtiles), dim3(256), 0, stream,
                            a, medium);
     return hipGetLastError() == hipSuccess ? 0 : -6;
 }
 
+// 16-bit rows that start on cache lines are written past the caches (gated 2048 x
+// 4096 x 2*14336: 211 against 216 us, 384 x 768 x 50176: 25 and 36 us); other
+// rows would leave parts of lines (333 x 768 x 50257: 28 against 26 us in
+// binary16, 57 against 38 in fp32), and fp32 gains nothing (233 against 239 us
+// without at 4096 x 8192 x 8192).
 template <int YT>
 int launch_type(const I8Args &a, bool gated, hipStream_t stream)
 {
-    return gated ? launch_form<YT, true>(a, stream) : launch_form<YT, false>(a, stream);
+    if constexpr (YT != Q8_T_F32)
+        if (a.y_stride * 2 % 128 == 0 && (uintptr_t)a.y % 128 == 0)
+            return gated ? launch_form<YT, true, true>(a, stream) : launch_form<YT, false, true>(a, stream);
+    return gated ? launch_form<YT, true, false>(a, stream) : launch_form<YT, false, false>(a, stream);
 }
 
 }  // namespace
