@@ -644,6 +644,7 @@ int i8_quantize_rows(const void *x, int x_type, int64_t x_row_stride, int8_t *q,
  *   ws       i8_workspace_bytes(m, k) bytes, 256-byte aligned, where x is not
  *            codes (else ignored); contents need not be initialised; not shared
  *            by calls that may run concurrently
+ * y must not overlap any input.
  * m, n >= 0, 0 < k <= 131040, k % 32 == 0; codes may be any int8 value, -128
  * included; row strides at most 4 MiB, m and n at most 2^27, m * n at most
  * 2^36 (Q8_E_UNSUPPORTED).

@@ -60,6 +60,17 @@ def test_sizes(q, m, v, t):
         _check(q, _logits(rng, m, v), t, tokens, n_top)
 
 
+@pytest.mark.parametrize("m,v,tops", [(1, 1300000, (0, 20, 64)), (2, 700001, (1, 64)),
+                                      (3, 400000, (5, 20, 40)), (70001, 37, (0, 5))])
+def test_many_parts_and_rows(q, m, v, tops):
+    """Rows in up to 64 parts, and more rows than one launch takes."""
+    rng = synth.rng("lpparts", str(m), str(v))
+    x = _logits(rng, m, v)
+    tokens = rng.integers(0, v, size=(m, 1)).astype(np.int32)
+    for n_top in tops:
+        _check(q, x, "bf16" if m == 3 else "fp32", tokens, n_top)
+
+
 @pytest.mark.parametrize("t", i8_ref.TYPES)
 @pytest.mark.parametrize("offset,pad", [(0, 1), (1, 0), (3, 5), (7, 8), (1, 7), (2, 3)])
 def test_row_starts(q, offset, pad, t):
