@@ -63,6 +63,7 @@ struct Rows {
             (void *)p.xf, 0, (m - 1) * (int)p.xf_stride + 16 * per, kBufferWord3);
 #pragma unroll
         for (int u = 0; u < kN; ++u) {
+            if (64 * kWaves * u >= m * per) break;
             const int i = threadIdx.x + 64 * kWaves * u;
             row[u] = i >= m * per ? kXlRows : (i >= per) + (i >= 2 * per) + (i >= 3 * per);
             at[u] = i - row[u] * per;
@@ -76,17 +77,20 @@ struct Rows {
     __device__ __forceinline__ void store(const StreamArgs &p, int per, uint8_t *xs, float *scale,
                                           uint32_t (*amax)[kXlRows])
     {
+        const int m = (int)p.a.m;
         if constexpr (XT == Q8_T_I8) {
 #pragma unroll
-            for (int u = 0; u < kN; ++u)
+            for (int u = 0; u < kN; ++u) {
+                if (64 * kWaves * u >= m * per) break;
                 if (row[u] < kXlRows) *(u32x4 *)(xs + 16 * (row[u] * per + at[u])) = r[u];
+            }
             if (threadIdx.x < p.a.m) scale[threadIdx.x] = p.a.x_scale[threadIdx.x];
         } else {
             constexpr int V = kVec<XT>;
-            const int m = (int)p.a.m;
             uint32_t b[kXlRows] = {};
 #pragma unroll
             for (int u = 0; u < kN; ++u) {
+                if (64 * kWaves * u >= m * per) break;
                 float v[V];
                 unpack16<XT>(r[u], v);
                 uint32_t c = 0;
@@ -112,6 +116,7 @@ struct Rows {
             if (threadIdx.x < m) scale[threadIdx.x] = of_row(threadIdx.x);
 #pragma unroll
             for (int u = 0; u < kN; ++u) {
+                if (64 * kWaves * u >= m * per) break;
                 if (row[u] == kXlRows) continue;
                 const RowCoder rc(of_row(row[u]));
                 float v[V];
