@@ -1,12 +1,12 @@
 // i8_stream.hip -- the 8-bit products with token and channel scales for few
 // token rows (decode, small batches), where HBM bounds the kernel, and for
 // small matrices, where the length of k does: no workgroup waits for another
-// and its four waves walk four parts of k.
+// and its waves walk interleaved parts of k.
 //
 // Work decomposition:
-//  * Workgroup = 4 waves, 16*NI weight rows x 16*MT tokens, all of k: the
+//  * Workgroup = 4 or 8 waves, 16*NI weight rows x 16*MT tokens, all of k: the
 //    waves take the 128-byte steps of k in turn (so a row's bytes are read in
-//    runs of 512) and their int32 sums are joined in LDS at the end.
+//    runs of 512 or 1024) and their int32 sums are joined in LDS at the end.
 //  * Each wave has a ring of stages of its own in LDS: the weight rows (and
 //    token rows) of a step are copied straight there (16-byte buffer loads in
 //    LDS DMA mode, 8 rows x 128 bytes each), so loads in flight cost no
@@ -26,7 +26,6 @@ namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;
 constexpr int kStep = 128;
 constexpr int kOut = 0x7fffff00;  // an offset past every resource: reads zero
 constexpr int kXlValues = 8192;   // XL: values of all token rows together
@@ -48,11 +47,12 @@ __device__ __forceinline__ void lds_barrier()
 }
 
 // The token rows as 16-byte pieces, `per` of them a row; thread t has pieces
-// t + 256 u.
-template <int XT>
+// t + 64 kWaves u.
+template <int XT, int kWaves>
 struct Rows {
     static constexpr int kBytes = XT == Q8_T_F32 ? 4 : XT == Q8_T_I8 ? 1 : 2;
     static constexpr int kN = kXlValues * kBytes / 16 / (64 * kWaves);
+    static_assert(kN > 0, "at least a piece per thread");
     u32x4 r[kN];
     int row[kN], at[kN];                   // kXlRows past the last piece
 
@@ -131,8 +131,8 @@ struct Rows {
     }
 };
 
-template <>
-struct Rows<-1> {
+template <int kWaves>
+struct Rows<-1, kWaves> {
     __device__ __forceinline__ void load(const StreamArgs &, int) {}
     __device__ __forceinline__ void store(const StreamArgs &, int, uint8_t *, float *,
                                           uint32_t (*)[kXlRows]) {}
@@ -141,7 +141,7 @@ struct Rows<-1> {
 // NI: 16-row weight tiles (in the gated form NI/2 of gate rows, then NI/2 of
 // the up rows of the same outputs).  MT: 16-token tiles.
 // XT: the type of token rows taken as given (XL), or -1.
-template <int NI, int MT, int XT, bool GATED>
+template <int NI, int MT, int kWaves, int XT, bool GATED>
 __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs p)
 {
     constexpr bool XL = XT >= 0;
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
     const int8_t *x = a.x + m0 * a.x_stride;
     const int w_bytes = (w_rows - 1) * w_stride + k;
 
-    // steps wave, wave + 4, ...; a step past the end loads zeros, so every
+    // steps wave, wave + kWaves, ...; a step past the end loads zeros, so every
     // wave has the same number of loads in flight
     auto issue = [&](int it, uint8_t *s) {
         const int st = it * kWaves + wave;
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
         issue(it + 2, s);
     };
 
-    // the scales this lane needs at the end: tiles wave, wave + 4, ...
+    // the scales this lane needs at the end: tiles wave, wave + kWaves, ...
     constexpr int kTiles = NI * MT;
     constexpr int kDone = GATED ? kTiles / 2 : kTiles;
     constexpr int kMine = (kDone + kWaves - 1) / kWaves;
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
         }
     }
     const int per = k * (XT == Q8_T_F32 ? 4 : XT == Q8_T_I8 ? 1 : 2) / 16;
-    Rows<XT> rows;
+    Rows<XT, kWaves> rows;
     rows.load(p, per);
     issue(0, ring0[wave]);
     issue(1, ring1[wave]);
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
     }
 
     // join the waves' sums: each wave its own ring slot, then wave w finishes
-    // tiles w, w + 4, ...  (zeros still in flight to the ring land first)
+    // tiles w, w + kWaves, ...  (zeros still in flight to the ring land first)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     v4i *join = (v4i *)ring0;                              // [kWaves][kTiles][64]
@@ -325,39 +325,56 @@ int64_t workgroups(const I8Args &a, bool gated, int ni, int mt)
     return (a.n + outs - 1) / outs * ((a.m + 16 * mt - 1) / (16 * mt));
 }
 
-template <int NI, int MT, int XT>
+template <int NI, int MT, int NW, int XT>
 int launch(const StreamArgs &p, bool gated, hipStream_t stream)
 {
     const int64_t by = (p.a.m + 16 * MT - 1) / (16 * MT), bx = workgroups(p.a, gated, NI, MT) / by;
     if (bx >= (1 << 24)) return Q8_E_UNSUPPORTED;
     const dim3 grid((unsigned)bx, (unsigned)by);
-    if (gated)
-        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, XT, true>), grid, dim3(64 * kWaves), 0, stream, p);
-    else
-        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, XT, false>), grid, dim3(64 * kWaves), 0, stream, p);
+    bool done = false;
+    if constexpr (NI > 1)            // (shape() gives the gated form two rows of tiles)
+        if (gated) {
+            hipLaunchKernelGGL((i8_stream_kernel<NI, MT, NW, XT, true>), grid, dim3(64 * NW), 0, stream, p);
+            done = true;
+        }
+    if (!done)
+        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, NW, XT, false>), grid, dim3(64 * NW), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -6;
 }
 
 // The smallest workgroups of which the device needs at most one per CU are the
-// fastest (a workgroup's time grows with its rows: at k = 4096 7.6 us for 32
-// weight rows x 16 tokens, 8.4 for 32 x 32, 10.6 for 32 x 64, 14.1 for
-// 64 x 64); 0 where even 64 x 64 ones are more.
+// fastest (a workgroup's time grows with its rows: at k = 4096, in 4 waves,
+// 7.6 us for 32 weight rows x 16 tokens, 8.4 for 32 x 32, 10.6 for 32 x 64,
+// 14.1 for 64 x 64); 0 where even 64 x 64 ones are more.
 struct Shape {
     int ni, mt;
 };
 
 Shape shape(const I8Args &a, bool gated)
 {
-    const Shape s[4] = {{2, 1}, {2, 2}, {2, 4}, {4, 4}};
-    for (int i = 0; i < 4; ++i)
-        if ((i == 0 || 8 * s[i].mt < a.m) && workgroups(a, gated, s[i].ni, s[i].mt) <= 256) return s[i];
+    const Shape s[5] = {{1, 1}, {2, 1}, {2, 2}, {2, 4}, {4, 4}};
+    for (int i = gated ? 1 : 0; i < 5; ++i)
+        if ((i < 2 || 8 * s[i].mt < a.m) && workgroups(a, gated, s[i].ni, s[i].mt) <= 256) return s[i];
     return {0, 0};
+}
+
+// Waves of the small shapes.  A turn of the ring is two steps per wave, 1024
+// values of k in 4 waves: past that 8 waves take half the turns (1 x 4096 x 4096
+// 7.5 -> 6.0 us, 1 x 8192 x 2048 11.8 -> 8.3, 16 x 8192 x 1024 13.5 -> 11.3),
+// up to it they only join more sums (1 x 768 x 2 x 2048 gated 4.0 -> 4.7).
+template <int NI, int MT, int XT>
+int launch_small(const StreamArgs &p, bool gated, hipStream_t stream)
+{
+    return p.a.k > 2 * 4 * kStep ? launch<NI, MT, 8, XT>(p, gated, stream)
+                                 : launch<NI, MT, 4, XT>(p, gated, stream);
 }
 
 template <int XT>
 int launch_rows(const StreamArgs &p, bool gated, hipStream_t stream)
 {
-    return shape(p.a, gated).ni ? launch<2, 1, XT>(p, gated, stream) : launch<4, 1, XT>(p, gated, stream);
+    const int ni = shape(p.a, gated).ni;
+    if (ni == 1) return launch_small<1, 1, XT>(p, gated, stream);
+    return ni ? launch_small<2, 1, XT>(p, gated, stream) : launch<4, 1, 4, XT>(p, gated, stream);
 }
 
 }  // namespace
@@ -377,13 +394,14 @@ int launch_i8_stream(const I8Args &a, const void *xf, int xf_type, int64_t xf_st
     if (xf && xf_type == Q8_T_BF16) return launch_rows<Q8_T_BF16>(p, gated, stream);
     if (xf) return launch_rows<Q8_T_I8>(p, gated, stream);
     const Shape s = shape(a, gated);
-    if (s.mt == 1) return launch<2, 1, -1>(p, gated, stream);
-    if (s.mt == 2) return launch<2, 2, -1>(p, gated, stream);
-    if (s.ni == 2) return launch<2, 4, -1>(p, gated, stream);
+    if (s.ni == 1) return launch_small<1, 1, -1>(p, gated, stream);
+    if (s.mt == 1) return launch_small<2, 1, -1>(p, gated, stream);
+    if (s.mt == 2) return launch_small<2, 2, -1>(p, gated, stream);
+    if (s.ni == 2) return launch<2, 4, 4, -1>(p, gated, stream);
     // HBM bounds it: 64 weight rows, all tokens at once where they are 64 or fewer
-    if (a.m <= 16) return launch<4, 1, -1>(p, gated, stream);
-    if (a.m <= 32) return launch<4, 2, -1>(p, gated, stream);
-    return launch<4, 4, -1>(p, gated, stream);
+    if (a.m <= 16) return launch<4, 1, 4, -1>(p, gated, stream);
+    if (a.m <= 32) return launch<4, 2, 4, -1>(p, gated, stream);
+    return launch<4, 4, 4, -1>(p, gated, stream);
 }
 
 }  // namespace q8
