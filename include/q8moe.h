@@ -655,7 +655,8 @@ int i8_quantize_rows(const void *x, int x_type, int64_t x_row_stride, int8_t *q,
  * [2*n_ff][k] (gate rows first, the layout of q8_0_up_gate_swiglu_batched) and
  * w_scale [2*n_ff],  h[t][j] = silu(g) * u = g / (1 + exp(-g)) * u  in fp32,
  * g and u the i8_matmul values (without bias) of rows j and n_ff + j, rounded
- * once to h's type.  Everything else as i8_matmul.
+ * once to h's type (for g below -87, where silu(g) is under 2^-118, h may be a
+ * zero).  Everything else as i8_matmul.
  */
 size_t i8_workspace_bytes(int64_t m, int64_t k);
 

@@ -381,7 +381,8 @@ TileGrid tile_grid(const I8Args &a, bool gated, int tile)
 {
     const int64_t cols = gated ? tile / 2 : tile;
     const int64_t tn = (a.n + cols - 1) / cols, tm = (a.m + tile - 1) / tile;
-    if (tn * tm >= ((int64_t)1 << 23)) return {0, 0, 0};
+    // (2^36 outputs are fewer than 2^24 tiles, and those below 2^32 threads)
+    if (tn * tm >= ((int64_t)1 << 24)) return {0, 0, 0};
     return {(int)tn, (int)tm, (int)(tn * tm)};
 }
 

@@ -15,6 +15,8 @@
 // 128 places are full, each candidate counts the larger ones (its rank) and the
 // first n_top stay.  Most 16-byte groups are dismissed by their maximum, which
 // the sums need anyway.
+#include <type_traits>
+
 #include "i8_device.h"
 #include "q8_i8.h"
 
@@ -52,13 +54,15 @@ __device__ __forceinline__ void stat_move(Stat &a, float r)
     a.r = r;
 }
 
-// One term; r2 = the reference's product, a.r the reference.
+// One term; r2 = the reference's product, a.r the reference.  LOW: x may be so
+// low that d is -infinity; else that makes w a NaN (0 * infinity).
+template <bool LOW>
 __device__ __forceinline__ void stat_add(Stat &a, float x, float r2)
 {
     const float d = fmaf(x, kL2E, -r2);
     const float e = __builtin_amdgcn_exp2f(d);
     a.s += e;
-    a.w = fmaf(e, fmaxf(d, -1e30f), a.w);           // no 0 * infinity
+    a.w = fmaf(e, LOW ? fmaxf(d, -1e30f) : d, a.w);
 }
 
 // A reduction over the wave's lanes by data-parallel-primitive moves (in rows
@@ -442,32 +446,54 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
     Given g = {-1, 0.0f};
     if (wk.parts == 1) g = given<T>(a, row, threadIdx.x);
     float lane_max = __builtin_nanf("");
+    bool low = false;                  // this wave has met a logit of -infinity or near
     for (int it = 0; it * W * turn < vecs; ++it) {
-        const int v0 = (it * W + wave) * turn;
-        float xv[kLoads][V], best[kLoads], r = st.r;
+        const int v0 = (it * W + wave) * turn, left = vecs - v0;
+        float xv[kLoads][V], best[kLoads];
 #pragma unroll
-        for (int u = 0; u < kLoads; ++u) unpack16<T>(raw[u], xv[u]);
+        for (int u = 0; u < kLoads; ++u) {
+            unpack16<T>(raw[u], xv[u]);
+            best[u] = -INFINITY;
+        }
         if ((it + 1) * W * turn < vecs) fetch(v0 + W * turn);    // lands during this turn
-        if (v0 + turn > vecs) {
+        if (left < turn) {
+            // no terms: lower than any reference, and d stays finite
 #pragma unroll
             for (int u = 0; u < kLoads; ++u)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    if (v0 + 64 * u + lane >= vecs) xv[u][j] = -INFINITY;
+                    if (64 * u + lane >= left) xv[u][j] = -2e38f;
         }
+        if (left > 0) {
+            float r = st.r;
 #pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-            best[u] = xv[u][0];
+            for (int u = 0; u < kLoads; ++u) {
+                best[u] = xv[u][0];
 #pragma unroll
-            for (int j = 1; j < V; ++j) best[u] = fmaxf(best[u], xv[u][j]);
-            r = fmaxf(r, best[u]);
+                for (int j = 1; j < V; ++j) best[u] = fmaxf(best[u], xv[u][j]);
+                r = fmaxf(r, best[u]);
+            }
+            stat_move(st, r);
+            const float r2 = r * kL2E;
+            auto terms = [&](auto with_low) {
+                Stat t = st;
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    if (64 * u >= left) break;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) stat_add<decltype(with_low)::value>(t, xv[u][j], r2);
+                }
+                return t;
+            };
+            // without the clamp of every term, 32 of 220 instructions, until a
+            // sum says that it is needed
+            Stat t = st;
+            if (!low) {
+                t = terms(std::false_type());
+                low = __ballot(t.w != t.w) != 0;
+            }
+            st = low ? terms(std::true_type()) : t;
         }
-        stat_move(st, r);
-        const float r2 = r * kL2E;
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u)
-#pragma unroll
-            for (int j = 0; j < V; ++j) stat_add(st, xv[u][j], r2);
         if (TOP) {
 #pragma unroll
             for (int u = 0; u < kLoads; ++u)
@@ -498,7 +524,7 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
     if (head + tail && wave == W - 1) {
         const float r = fmaxf(st.r, edge);
         stat_move(st, r);
-        stat_add(st, edge, r * kL2E);
+        stat_add<true>(st, edge, r * kL2E);
         if (TOP) top.offer(edge, (uint32_t)(begin + edge_i), lane < head + tail, lane);
     }
 
