@@ -1,5 +1,5 @@
 // logprob.hip -- log probabilities of given tokens, log sum exp, entropy and the
-// largest logits of each row, in one pass over the logits (HBM bounds it).
+// largest logits of each row, in one pass over the logits.
 //
 // A workgroup takes a row, or a part of one where there are few rows; the parts
 // are joined by a second launch.  Every lane keeps a running (reference r, S =
@@ -10,11 +10,16 @@
 // The largest n_top logits: every wave keeps candidates of its own, (value,
 // lowest index first) as one 64-bit key, in LDS, and the key that a logit has to
 // pass.  After turns 1, 2, 4, 8, ... the workgroup sets a common bound: the
-// n_top-th largest of its 256 lanes' (or quads of lanes') maxima so far, which
+// n_top-th largest of the maxima so far of 64 or 256 groups of its lanes, which
 // n_top logits reach and few more, so few logits ever get in.  When a wave's
 // 128 places are full, each candidate counts the larger ones (its rank) and the
 // first n_top stay.  Most 16-byte groups are dismissed by their maximum, which
 // the sums need anyway.
+//
+// Bounds: HBM for long rows without a list (512 x 262144 bfloat16 41.5 us, 6.5
+// TB/s), the vector instructions with one (8 per logit and 400 per wave for a
+// list of 20, 16-bit types: 1021 x 50257 bfloat16 25.5 us, 4.0 TB/s; 20 without
+// the list), the chain of launch, loads and joins for few rows (1 x 32000 8 us).
 #include <type_traits>
 
 #include "i8_device.h"
@@ -27,6 +32,7 @@ namespace {
 constexpr float kL2E = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr int kPlaces = 128;      // candidates per wave
 constexpr int kMaxParts = 64;
+constexpr int kShortTop = 24;     // alternatives of a short list
 constexpr int kLoads = 4;         // 16-byte loads per lane and turn
 
 // r: the largest logit seen, or -1e38: x L stays finite beside it.
@@ -124,8 +130,19 @@ __device__ __forceinline__ uint32_t row_move(uint32_t v)
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, Ctrl, 0xf, 0xf, false);
 }
 
-// The n-th largest of 256 keys, four per lane, its low half cut (0: fewer than
-// n keys are not 0).
+// The n-th largest of 64 keys, one per lane, its low half cut (0: fewer than n
+// keys are not 0).
+__device__ __forceinline__ uint32_t nth_key(uint32_t key, int n)
+{
+    uint32_t t = 0;
+    for (int b = 31; b >= 16; --b) {
+        const uint32_t c = t | (1u << b);
+        if (__popcll(__ballot(key >= c)) >= n) t = c;
+    }
+    return t;
+}
+
+// The same of 256 keys, four per lane.
 __device__ __forceinline__ uint32_t nth_key(u32x4 key, int n)
 {
     uint32_t t = 0;
@@ -139,7 +156,8 @@ __device__ __forceinline__ uint32_t nth_key(u32x4 key, int n)
 }
 
 // f(rank, key) for the first n of `count` different keys in LDS (0: none), by
-// a whole workgroup: eight lanes count the larger ones of each.
+// a whole workgroup: eight lanes count the larger ones of each, two at a time
+// (what lies behind the last key, of an even number of places, is not counted).
 template <class F>
 __device__ __forceinline__ void by_rank(const uint64_t *keys, int count, int n, int threads, F f)
 {
@@ -148,7 +166,12 @@ __device__ __forceinline__ void by_rank(const uint64_t *keys, int count, int n, 
         const int c = c0 + (threadIdx.x >> 3);
         const uint64_t k = c < count ? keys[c] : 0;
         int rank = 0;
-        for (int j = sub; j < count; j += 8) rank += keys[j] > k;
+#pragma unroll 4
+        for (int j = 2 * sub; j < count; j += 16) {
+            const ulonglong2 o = *(const ulonglong2 *)(keys + j);
+            rank += o.x > k;
+            rank += j + 1 < count && o.y > k;
+        }
         rank += (int)row_move<0xb1>((uint32_t)rank);     // quad_perm:[1,0,3,2]
         rank += (int)row_move<0x4e>((uint32_t)rank);     // quad_perm:[2,3,0,1]
         rank += (int)row_move<0x141>((uint32_t)rank);    // row_half_mirror
@@ -429,40 +452,42 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
         top.init(places[wave], a.n_top);
         pend.init(pend_v[wave], pend_i[wave]);
     }
-    // a turn: kLoads x 64 vectors per wave; every wave makes the same number
-    const int turn = 64 * kLoads;
+    // a turn: kLoads x 64 vectors per wave, 64 of each wave in turn, so that a
+    // short row or last turn is spread over the waves; every wave makes the same
+    // number of turns
+    constexpr int kPart = 64 * W, kTurn = kPart * kLoads;
     u32x4 raw[kLoads];
     auto fetch = [&](int v0) {
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
             // past the end the last vector again, dismissed below
-            const int v = min(v0 + 64 * u + lane, vecs - 1);
+            const int v = min(v0 + kPart * u + lane, vecs - 1);
             raw[u] = __builtin_nontemporal_load((const u32x4 *)(x + (int64_t)v * V));
         }
     };
     const int edge_i = lane < head ? lane : lane + vecs * V;
     const float edge = lane < head + tail && wave == W - 1 ? (float)x0[edge_i] : -INFINITY;
-    if (vecs > 0) fetch(wave * turn);
+    if (vecs > 0) fetch(64 * wave);
     Given g = {-1, 0.0f};
     if (wk.parts == 1) g = given<T>(a, row, threadIdx.x);
     float lane_max = __builtin_nanf("");
     bool low = false;                  // this wave has met a logit of -infinity or near
-    for (int it = 0; it * W * turn < vecs; ++it) {
-        const int v0 = (it * W + wave) * turn, left = vecs - v0;
+    for (int it = 0; it * kTurn < vecs; ++it) {
+        const int v0 = it * kTurn + 64 * wave, left = vecs - v0;
         float xv[kLoads][V], best[kLoads];
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
             unpack16<T>(raw[u], xv[u]);
             best[u] = -INFINITY;
         }
-        if ((it + 1) * W * turn < vecs) fetch(v0 + W * turn);    // lands during this turn
-        if (left < turn) {
+        if ((it + 1) * kTurn < vecs) fetch(v0 + kTurn);    // lands during this turn
+        if (left < kPart * (kLoads - 1) + 64) {
             // no terms: lower than any reference, and d stays finite
 #pragma unroll
             for (int u = 0; u < kLoads; ++u)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    if (64 * u + lane >= left) xv[u][j] = -2e38f;
+                    if (kPart * u + lane >= left) xv[u][j] = -2e38f;
         }
         if (left > 0) {
             float r = st.r;
@@ -479,7 +504,7 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
                 Stat t = st;
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
-                    if (64 * u >= left) break;
+                    if (kPart * u >= left) break;
 #pragma unroll
                     for (int j = 0; j < V; ++j) stat_add<decltype(with_low)::value>(t, xv[u][j], r2);
                 }
@@ -497,7 +522,7 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
         if (TOP) {
 #pragma unroll
             for (int u = 0; u < kLoads; ++u)
-                lane_max = fmaxf(lane_max, v0 + 64 * u + lane < vecs ? best[u] : __builtin_nanf(""));
+                lane_max = fmaxf(lane_max, kPart * u + lane < left ? best[u] : __builtin_nanf(""));
             if ((it & (it + 1)) == 0) {            // turns 1, 2, 4, 8, ...
                 uint32_t mine = value_key(lane_max);
                 if (W == 16) {                     // 256 quads
@@ -508,13 +533,19 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
                 uint32_t *set = bounds[__builtin_popcount(it) & 1];
                 if (W == 4 || lane % 4 == 0) set[threadIdx.x / (W / 4)] = mine;
                 __syncthreads();
-                const uint32_t all = nth_key(*(const u32x4 *)(set + 4 * lane), a.n_top);
+                // (64 groups do for a short list: 20 of them let in 24 logits
+                // where 20 of 256 let in 21, at a quarter of the work: 2048 x
+                // 32000 bfloat16 with a list of 20 34.9 -> 31.0 us)
+                const u32x4 four = {set[lane], set[64 + lane], set[128 + lane], set[192 + lane]};
+                const uint32_t all = a.n_top <= kShortTop
+                                         ? nth_key(max(max(four.x, four.y), max(four.z, four.w)), a.n_top)
+                                         : nth_key(four, a.n_top);
                 const uint64_t t = ((uint64_t)all << 32) - 1;
                 if (all && t > top.thr) top.set(t);
             }
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
-                const int v = v0 + 64 * u + lane;
+                const int v = v0 + kPart * u + lane;
                 const uint64_t in = __ballot(v < vecs && !(best[u] < top.least));
                 if (in) pend.push(in, repack16<T>(xv[u]), v, begin + head, top, lane);
             }
@@ -531,7 +562,7 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
     st = wave_join(st);
     if (lane == 0) part[wave] = st;
     if (TOP) {
-        if (top.count > a.n_top) top.compact(lane);
+        if (top.count > kLogprobMaxTop) top.compact(lane);       // what `merged` has room for
         wave_lds_sync();
         if (lane == 0) counts[wave] = top.count;
     }
@@ -594,7 +625,7 @@ __global__ __launch_bounds__(256) void logprob_join_kernel(const LogprobArgs a, 
     if (a.n_top > 0) {
         const int each = (a.n_top + wk.parts - 1) / wk.parts;
         const uint32_t v = lane < wk.parts ? (uint32_t)(tops[lane * a.n_top + each - 1] >> 32) : 0;
-        t = nth_key((u32x4){v, 0, 0, 0}, (a.n_top + each - 1) / each);
+        t = nth_key(v, (a.n_top + each - 1) / each);
         if (tid == 0) count = 0;
         __syncthreads();
     }

@@ -122,6 +122,29 @@ def test_masked_rows(q, v, t):
     assert float(out.entropy[1]) == 0 and float(out.lse[1]) == -np.inf
 
 
+@pytest.mark.parametrize("t", ["fp32", "bf16"])
+@pytest.mark.parametrize("v", [1000, 12289, 50257, 262144])
+def test_low_logits_on_the_way(q, v, t):
+    """-infinity, and values whose product with log2 e overflows, that first come
+    up late in a row, in one place of it or everywhere behind it, beside small
+    and large references."""
+    rng = synth.rng("lplow", str(v))
+    x = _logits(rng, 8, v)
+    x[0, v - 2] = -np.inf
+    x[1, v // 2:] = -np.inf
+    x[2, v // 3] = -3.1e38
+    x[3, 2 * v // 3:] = -2.5e38
+    x[4] = x[4] * 1e29 + 1e30
+    x[4, v // 2] = -np.inf
+    x[5, :-1] = -2e38                 # a reference far above everything else
+    x[6] = -2.2e38                    # nothing above the first reference
+    x[6, v // 5] = -np.inf
+    x[7, ::7] = -1.5e38
+    tokens = np.array([[0, v // 2]] * 8, np.int32)
+    for n_top in (0, 3, 20, 25, 64):
+        _check(q, x, t, tokens, n_top)
+
+
 @pytest.mark.parametrize("t", i8_ref.TYPES)
 @pytest.mark.parametrize("v", [64, 3000, 50257, 200000])
 def test_nan_and_infinity(q, v, t):
