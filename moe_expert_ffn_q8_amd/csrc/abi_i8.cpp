@@ -64,7 +64,7 @@ int i8_product(const void *x, int x_type, int64_t x_row_stride, const float *x_s
     if (!codes && (!ws || ws_bytes < i8_workspace_bytes(m, k))) return Q8_E_WORKSPACE;
     if (!codes && !aligned(ws, 256)) return Q8_E_ALIGN;
     a.x = (const int8_t *)x; a.x_scale = x_scale; a.x_stride = x_row_stride;
-    if (q8::i8_inline_ok(m, k))
+    if (q8::i8_inline_ok(a, gated))
         return hip_status(q8::launch_i8_stream(a, x, x_type, x_row_stride * type_bytes(x_type),
                                                gated, st));
     if (!codes) {

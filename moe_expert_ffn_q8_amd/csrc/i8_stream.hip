@@ -30,7 +30,10 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;
 constexpr int kOut = 0x7fffff00;  // an offset past every resource: reads zero
-constexpr int kXlValues = 8192;   // XL: values of all token rows together
+// XL: values of all token rows together, in the kernels of one workgroup per CU
+// and in those of many (NI = 4; more there would leave room for one per CU, and
+// 262144 x 2048 at one token would take 98 us for 80).
+template <int NI> constexpr int kXlValues = NI == 4 ? 8192 : 16384;
 constexpr int kXlRows = 4;
 
 struct StreamArgs {
@@ -50,10 +53,10 @@ __device__ __forceinline__ void lds_barrier()
 
 // The token rows as 16-byte pieces, `per` of them a row; thread t has pieces
 // t + 64 kWaves u.
-template <int XT, int kWaves>
+template <int XT, int kWaves, int kValues>
 struct Rows {
     static constexpr int kBytes = XT == Q8_T_F32 ? 4 : XT == Q8_T_I8 ? 1 : 2;
-    static constexpr int kN = kXlValues * kBytes / 16 / (64 * kWaves);
+    static constexpr int kN = kValues * kBytes / 16 / (64 * kWaves);
     static_assert(kN > 0, "at least a piece per thread");
     u32x4 r[kN];
     int row[kN], at[kN];                   // kXlRows past the last piece
@@ -133,8 +136,8 @@ struct Rows {
     }
 };
 
-template <int kWaves>
-struct Rows<-1, kWaves> {
+template <int kWaves, int kValues>
+struct Rows<-1, kWaves, kValues> {
     __device__ __forceinline__ void load(const StreamArgs &, int) {}
     __device__ __forceinline__ void store(const StreamArgs &, int, uint8_t *, float *,
                                           uint32_t (*)[kXlRows]) {}
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
     static_assert(!XL || MT == 1, "few rows");
     __shared__ __align__(16) uint8_t ring0[kWaves][kStage];
     __shared__ __align__(16) uint8_t ring1[kWaves][kStage];
-    __shared__ __align__(16) uint8_t xs[XL ? kXlValues : 16];
+    __shared__ __align__(16) uint8_t xs[XL ? kXlValues<NI> : 16];
     __shared__ float xl_scale[kXlRows];
     __shared__ uint32_t xl_amax[kWaves][kXlRows];
 
@@ -261,7 +264,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
         }
     }
     const int per = k * (XT == Q8_T_F32 ? 4 : XT == Q8_T_I8 ? 1 : 2) / 16;
-    Rows<XT, kWaves> rows;
+    Rows<XT, kWaves, kXlValues<NI>> rows;
     rows.load(p, per);
     issue(0, ring0[wave]);
     issue(1, ring1[wave]);
@@ -383,7 +386,14 @@ int launch_rows(const StreamArgs &p, bool gated, hipStream_t stream)
 
 bool i8_stream_ok(const I8Args &a, bool gated) { return a.m <= 64 || shape(a, gated).ni != 0; }
 
-bool i8_inline_ok(int64_t m, int64_t k) { return m <= kXlRows && m * k <= kXlValues; }
+// (graph times with 16384 values against a quantizer launch: 1 x 14336 x 4096
+// bfloat16 13.8 and 16.8 us, fp32 15.0 and 19.2, 2 x 8192 x 2048 9.4 and 10.4, but
+// 4 x 4096 x 2048 fp32 9.4 and 8.0)
+bool i8_inline_ok(const I8Args &a, bool gated)
+{
+    const int64_t values = a.m <= 2 && shape(a, gated).ni ? kXlValues<1> : kXlValues<4>;
+    return a.m <= kXlRows && a.m * a.k <= values;
+}
 
 int launch_i8_stream(const I8Args &a, const void *xf, int xf_type, int64_t xf_stride, bool gated,
                      hipStream_t stream)

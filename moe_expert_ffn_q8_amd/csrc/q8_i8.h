@@ -36,7 +36,7 @@ int launch_i8_quantize(const void *x, int type, int64_t x_stride, int8_t *q, int
 // most 64 rows.  With xf the token rows are taken as given (xf_type, Q8_T_I8
 // included; bytes per row xf_stride) where i8_inline_ok, and a.x is not read.
 bool i8_stream_ok(const I8Args &a, bool gated);
-bool i8_inline_ok(int64_t m, int64_t k);
+bool i8_inline_ok(const I8Args &a, bool gated);
 int launch_i8_stream(const I8Args &a, const void *xf, int xf_type, int64_t xf_stride, bool gated,
                      hipStream_t stream);
 

@@ -177,6 +177,31 @@ def test_large(q, m, rows, k, t):
         assert bool((buf == 5.5).all())
 
 
+@pytest.mark.parametrize("t", i8_ref.TYPES + ("codes",))
+@pytest.mark.parametrize("n", [70, 5000, 20000])
+def test_few_long_rows(q, n, t):
+    """Float rows of up to 16384 values together, and just more, have the bits of
+    the quantizer's codes; so have codes wherever they are read from."""
+    import torch
+    for m, k in ((1, 8192), (1, 8224), (1, 16384), (1, 16416), (2, 4096), (2, 4128), (2, 8192),
+                 (2, 8224), (3, 2720), (3, 2752), (4, 2048), (4, 2080), (4, 4096), (5, 1632)):
+        rng, cx, sx, cw, sw = _operands(m, n, k, "few")
+        w, ws = to_gpu(cw), to_gpu(sw)
+        if t == "codes":
+            codes, scale = to_gpu(cx), to_gpu(sx)
+            x, kw = codes, {"x_scale": scale}
+        else:
+            x, _ = _typed(rng.normal(size=(m, k)) * np.arange(1, m + 1)[:, None], t)
+            codes, scale = q.i8_quantize_rows(x)
+            kw = {"ws": q.i8_workspace(m, k, "cuda")}
+        # (eight rows are beyond the form that quantizes inside)
+        many = codes.repeat(8, 1), scale.repeat(8)
+        for fn in (q.i8_matmul, q.i8_up_gate_swiglu):
+            y = fn(x, w, ws, **kw)
+            z = fn(many[0], w, ws, x_scale=many[1])
+            assert torch.equal(y, z[:m]), (fn.__name__, m, k)
+
+
 @pytest.mark.parametrize("m", [1, 3, 16, 40, 130, 300])
 @pytest.mark.parametrize("t", i8_ref.TYPES)
 def test_float_activations(q, m, t):
