@@ -935,13 +935,11 @@ _ACTS = {**_FLOATS, **_INT8}
 
 
 def _rows(t, name, types):
-    """(type, row stride, rows, columns) of a 2-D GPU tensor whose rows are
-    contiguous."""
+    """(type, row stride, rows, columns) of a 2-D tensor whose rows are
+    contiguous (where it lies: _on)."""
     code = types.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: {t.dtype}, expected one of {[str(d) for d in types]}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a GPU tensor")
     try:
         rows, cols = t.shape
         stride, step = t.stride()
@@ -953,34 +951,30 @@ def _rows(t, name, types):
 
 
 def _vector(t, n, dtype, name):
-    """Address of a contiguous GPU tensor of n elements."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    """Address of a contiguous tensor of n elements (where it lies: _on)."""
+    if t.dtype is not dtype or not t.is_contiguous():
         _need(t, dtype, name)
     if t.numel() != n:
         raise ValueError(f"{name}: {t.numel()} elements, expected {n}")
     return t.data_ptr()
 
 
-def _on(device, *ts):
-    """Every tensor of a call on `device`."""
+def _on(x, name, *ts):
+    """The device of x, a GPU, where every other tensor of the call has to be."""
+    device = x.device
+    if not x.is_cuda:
+        raise ValueError(f"{name}: must be a GPU tensor")
     for t in ts:
         if t is not None and t.device != device:
             raise ValueError(f"tensors on several devices: {device}, {t.device}")
+    return device
 
 
-def _enqueue(name, fn, device, *args):
-    """fn(*args, stream) on the device (made current for the call if it is not)
-    and its current stream.  (torch.cuda.current_stream() builds a Stream object
-    at 2 us a call; the raw handle is read in 0.1.)"""
-    index = device.index
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch._C._cuda_getDevice():
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
-    if rc != 0:
-        raise Q8Error(name, rc)
+# The device that is current and the handle of a device's current stream.
+# (torch.cuda.current_stream() builds a Stream object at 2 us a call; these take
+# 0.1.)  A call for another device makes it current and starts again.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def i8_quantize_rows(x, q=None, scale=None):
@@ -999,10 +993,14 @@ def i8_quantize_rows(x, q=None, scale=None):
     if (q_rows, q_k) != (n_rows, k):
         raise ValueError(f"q: shape {(q_rows, q_k)}, expected {(n_rows, k)}")
     scale_p = _vector(scale, n_rows, torch.float32, "scale")
-    device = x.device
-    _on(device, q, scale)
-    _enqueue("i8_quantize_rows", _lib.i8_quantize_rows, device, x.data_ptr(), xt, xs, q.data_ptr(),
-             qs, scale_p, n_rows, k)
+    index = _on(x, "x", q, scale).index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return i8_quantize_rows(x, q, scale)
+    rc = _lib.i8_quantize_rows(x.data_ptr(), xt, xs, q.data_ptr(), qs, scale_p, n_rows, k,
+                               _raw_stream(index))
+    if rc != 0:
+        raise Q8Error("i8_quantize_rows", rc)
     return q, scale
 
 
@@ -1024,7 +1022,6 @@ def _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated):
     if wk != k:
         raise ValueError(f"w: rows of {wk} codes, x has {k}")
     w_scale_p = _vector(w_scale, n, torch.float32, "w_scale")
-    device = x.device
     x_scale_p = bias_p = ws_p = None
     ws_bytes = 0
     if xt == 3:
@@ -1037,25 +1034,29 @@ def _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated):
         if ws is not None:
             ws_bytes = ws.numel()
             ws_p = _vector(ws, ws_bytes, torch.uint8, "ws")
-            _on(device, ws)
     if gated:
         if n % 2:
             raise ValueError(f"w: {n} rows, expected gate and up rows of one number")
         n //= 2
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=device)
+        out = torch.empty((m, n), dtype=dtype, device=x.device)
     yt, ys, y_rows, y_cols = _rows(out, "h" if gated else "y", _FLOATS)
     if y_rows != m or y_cols != n:
         raise ValueError(f"{'h' if gated else 'y'}: shape {(y_rows, y_cols)}, expected {(m, n)}")
     if bias is not None:
         bias_p = _vector(bias, n, torch.float32, "bias")
-    _on(device, w, w_scale, x_scale, bias, out)
+    index = _on(x, "x", w, w_scale, x_scale, bias, out, ws if ws_p else None).index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated)
     if gated:
-        _enqueue(name, fn, device, x.data_ptr(), xt, xs, x_scale_p, w.data_ptr(), wst, w_scale_p,
-                 out.data_ptr(), yt, ys, n, k, m, ws_p, ws_bytes)
+        rc = fn(x.data_ptr(), xt, xs, x_scale_p, w.data_ptr(), wst, w_scale_p, out.data_ptr(), yt, ys,
+                n, k, m, ws_p, ws_bytes, _raw_stream(index))
     else:
-        _enqueue(name, fn, device, x.data_ptr(), xt, xs, x_scale_p, w.data_ptr(), wst, w_scale_p,
-                 bias_p, out.data_ptr(), yt, ys, n, k, m, ws_p, ws_bytes)
+        rc = fn(x.data_ptr(), xt, xs, x_scale_p, w.data_ptr(), wst, w_scale_p, bias_p,
+                out.data_ptr(), yt, ys, n, k, m, ws_p, ws_bytes, _raw_stream(index))
+    if rc != 0:
+        raise Q8Error(name, rc)
     return out
 
 
@@ -1122,9 +1123,8 @@ def logprob_rows(logits, tokens=None, n_top=0, ws=None, out=None):
         if len(shape) not in (1, 2) or shape[0] != m:
             raise ValueError(f"tokens: shape {tuple(shape)}, expected [{m}] or [{m}][n_given]")
         n_given = 1 if len(shape) == 1 else shape[1]
-    device = logits.device
     if out is None:
-        out = logprob_outputs(m, n_given, n_top, device)
+        out = logprob_outputs(m, n_given, n_top, logits.device)
     given_p = ids_p = top_p = ws_p = None
     ws_bytes = 0
     if (n_given and out.logprob is None) or (n_top and (out.top_ids is None or out.top_logprobs is None)):
@@ -1139,9 +1139,15 @@ def logprob_rows(logits, tokens=None, n_top=0, ws=None, out=None):
     if ws is not None:
         ws_bytes = ws.numel()
         ws_p = _vector(ws, ws_bytes, torch.uint8, "ws")
-    _on(device, tokens, ws, *out)
-    _enqueue("logprob_rows", _lib.logprob_rows, device, logits.data_ptr(), t, stride, _ptr(tokens),
-             n_given, given_p, lse_p, entropy_p, ids_p, top_p, m, n_vocab, n_top, ws_p, ws_bytes)
+    index = _on(logits, "logits", tokens, ws, *out).index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return logprob_rows(logits, tokens, n_top, ws, out)
+    rc = _lib.logprob_rows(logits.data_ptr(), t, stride, None if tokens is None else tokens.data_ptr(),
+                           n_given, given_p, lse_p, entropy_p, ids_p, top_p, m, n_vocab, n_top, ws_p,
+                           ws_bytes, _raw_stream(index))
+    if rc != 0:
+        raise Q8Error("logprob_rows", rc)
     return out
 
 
