@@ -127,7 +127,7 @@ __device__ __forceinline__ void store_out(void *y, int64_t i, float v)
     ((typename Elem<T>::type *)y)[i] = round_out<T>(v);
 }
 
-// Two values of a 16-bit type in a dword (bfloat16: one instruction for both).
+// Two values of a 16-bit type in a dword (one instruction for both).
 template <int T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -136,26 +136,25 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
         typedef __bf16 e2 __attribute__((ext_vector_type(2)));
         return __builtin_bit_cast(uint32_t, __builtin_convertvector(((f2){lo, hi}), e2));
     } else if constexpr (T == Q8_T_F16) {
-        return (uint32_t)__builtin_bit_cast(uint16_t, round_out<T>(lo)) |
-               (uint32_t)__builtin_bit_cast(uint16_t, round_out<T>(hi)) << 16;
+        typedef _Float16 e2 __attribute__((ext_vector_type(2)));
+        asm("" : "+v"(lo), "+v"(hi));              // (as in round_out)
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(((f2){lo, hi}), e2));
     } else
         return 0;
 }
 
-// 16 bytes of outputs at element i, the first `left` elements of them (element
-// alignment is enough); STREAM: past the caches.
+// 16 bytes of outputs, the first `left` elements of them (element alignment is
+// enough); STREAM: past the caches.
 template <int T, bool STREAM>
-__device__ __forceinline__ void store16(void *y, int64_t i, u32x4 v, int left)
+__device__ __forceinline__ void store16(uint8_t *y, u32x4 v, int left)
 {
-    typedef typename Elem<T>::type E;
     typedef u32x4 __attribute__((aligned(2))) u32x4_any;
     constexpr int V = kVec<T>;
-    u32x4_any *to = (u32x4_any *)((E *)y + i);
     if (left >= V) {
         if constexpr (STREAM)
-            __builtin_nontemporal_store((u32x4_any)v, to);
+            __builtin_nontemporal_store((u32x4_any)v, (u32x4_any *)y);
         else
-            *to = v;
+            *(u32x4_any *)y = v;
         return;
     }
     const uint32_t d[4] = {v.x, v.y, v.z, v.w};
@@ -163,9 +162,9 @@ __device__ __forceinline__ void store16(void *y, int64_t i, u32x4 v, int left)
     for (int r = 0; r < V - 1; ++r)
         if (r < left) {
             if constexpr (T == Q8_T_F32)
-                ((uint32_t *)y)[i + r] = d[r];
+                ((uint32_t *)y)[r] = d[r];
             else
-                ((uint16_t *)y)[i + r] = (uint16_t)(d[r / 2] >> (16 * (r & 1)));
+                ((uint16_t *)y)[r] = (uint16_t)(d[r / 2] >> (16 * (r & 1)));
         }
 }
 

@@ -259,6 +259,12 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
     static_assert(kWaves <= 2 * kPerX + kPerW && 2 * 4 <= kStep, "fits");
     uint8_t *turn = wave < kPerX ? x0 + wave * 4096
                     : wave < 2 * kPerX ? x1 + (wave - kPerX) * 4096 : w0 + (wave - 2 * kPerX) * 4096;
+    // a lane's place in the wave's outputs: row o_row (+ 64 / kChunks per store),
+    // 16 bytes from column o_col on
+    const int o_row = lane / kChunks, o_col = lane % kChunks * (16 / kES);
+    const int rows_left = x_rows - wm * MI * 32 - o_row, cols_left = w_rows - wn * kWaveCols - o_col;
+    const int64_t y_bytes = a.y_stride * kES;
+    uint8_t *y = (uint8_t *)a.y + (m0 + wm * MI * 32 + o_row) * y_bytes + (n0 + wn * kWaveCols + o_col) * kES;
     auto outputs = [&](auto with_bias) {
         constexpr bool biased = decltype(with_bias)::value;
 #pragma unroll
@@ -298,12 +304,11 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
                 wave_lds_sync();
 #pragma unroll
                 for (int e = 0; e < kChunks / 2; ++e) {
-                    const int row = e * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
+                    const int up = e * (64 / kChunks), row = up + o_row, c = lane % kChunks;
                     const u32x4 o = *(const u32x4 *)(turn + row * 128 + 16 * (c ^ ((row >> 1) & 7)));
-                    const int64_t t = m0 + (wm * MI + j) * 32 + row;
-                    const int64_t n = n0 + wn * kWaveCols + 32 * i0 + c * (16 / kES);
-                    if (t < a.m && n < a.n)
-                        store16<YT, STREAM>(a.y, t * a.y_stride + n, o, (int)min((int64_t)8, a.n - n));
+                    if (32 * j + up < rows_left && 32 * i0 < cols_left)
+                        store16<YT, STREAM>(y + (32 * j + up) * y_bytes + 32 * i0 * kES, o,
+                                            cols_left - 32 * i0);
                 }
                 wave_lds_sync();
             }
