@@ -17,9 +17,9 @@
 // the sums need anyway.
 //
 // Bounds: HBM for long rows without a list (512 x 262144 bfloat16 41.5 us, 6.5
-// TB/s), the vector instructions with one (8 per logit and 400 per wave for a
-// list of 20, 16-bit types: 1021 x 50257 bfloat16 25.5 us, 4.0 TB/s; 20 without
-// the list), the chain of launch, loads and joins for few rows (1 x 32000 8 us).
+// TB/s), the vector instructions with one (7 to 8 per logit and 800 per wave for
+// a list of 20: 1021 x 50257 bfloat16 24 us, 4.3 TB/s; 20 us without the list),
+// the chain of launch, loads and joins for few rows (1 x 32000 8 us).
 #include <type_traits>
 
 #include "i8_device.h"
@@ -481,7 +481,8 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
             best[u] = -INFINITY;
         }
         if ((it + 1) * kTurn < vecs) fetch(v0 + kTurn);    // lands during this turn
-        if (left < kPart * (kLoads - 1) + 64) {
+        const bool full = left >= kPart * (kLoads - 1) + 64;
+        if (!full) {
             // no terms: lower than any reference, and d stays finite
 #pragma unroll
             for (int u = 0; u < kLoads; ++u)
@@ -520,9 +521,14 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
             st = low ? terms(std::true_type()) : t;
         }
         if (TOP) {
+            if (full) {
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u)
-                lane_max = fmaxf(lane_max, kPart * u + lane < left ? best[u] : __builtin_nanf(""));
+                for (int u = 0; u < kLoads; ++u) lane_max = fmaxf(lane_max, best[u]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u)
+                    lane_max = fmaxf(lane_max, kPart * u + lane < left ? best[u] : __builtin_nanf(""));
+            }
             if ((it & (it + 1)) == 0) {            // turns 1, 2, 4, 8, ...
                 uint32_t mine = value_key(lane_max);
                 if (W == 16) {                     // 256 quads
@@ -546,7 +552,8 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 const int v = v0 + kPart * u + lane;
-                const uint64_t in = __ballot(v < vecs && !(best[u] < top.least));
+                uint64_t in = __ballot(!(best[u] < top.least));
+                if (!full) in &= __ballot(v < vecs);
                 if (in) pend.push(in, repack16<T>(xv[u]), v, begin + head, top, lane);
             }
         }
