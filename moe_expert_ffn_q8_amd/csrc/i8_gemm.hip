@@ -8,7 +8,7 @@
 // matrix cores, and they by power on codes that are not mostly zeros: 8192^3
 // 441 us, 2.5 POPS; gated 2048 x 4096 x 2*14336 206 to 211 us, 2.3 POPS at 1.8
 // GHz; 512 x 4096 x 14336 30 us on part of the device.  With few steps the
-// start and end of each tile are most of the time: 333 x 768 x 50257 25 to 27 us,
+// start and end of each tile are most of the time: 333 x 768 x 50257 25 to 28 us,
 // of which the outputs are 10.
 //
 // Work decomposition:
