@@ -35,16 +35,22 @@ constexpr int kMaxParts = 64;
 constexpr int kShortTop = 24;     // alternatives of a short list
 constexpr int kLoads = 4;         // 16-byte loads per lane and turn
 
-// r: the largest logit seen, or -1e38: x L stays finite beside it.
+// r: the largest logit seen, kLow at least.  The terms are formed beside the
+// rounded product r L, which up to |r| = 2^24 is within 1 of r L, so that S counts
+// each largest logit as 1/2 to 2; the rounding grows with r, and beside a
+// reference of -2.5e9 (a mask of -1e9 over a temperature of 0.4) the terms would be
+// 2^110 and W overflow.  A mask below kLow adds nothing, and a row whose maximum
+// is not between kLow and -kLow is left to slow_stat.
+constexpr float kLow = -0x1p24f;
+
 struct Stat {
     float r, s, w;
 };
 
-__device__ __forceinline__ Stat stat_zero() { return {-1e38f, 0.0f, 0.0f}; }
+__device__ __forceinline__ Stat stat_zero() { return {kLow, 0.0f, 0.0f}; }
 
 // Both references as the rounded products that the terms were formed with (a
-// fused multiply-add would put the rounding of r L into every move, and at
-// -1e38 overflow the factor).
+// fused multiply-add would put the rounding of r L into every move).
 __device__ __forceinline__ void stat_move(Stat &a, float r)
 {
     float d;
@@ -323,25 +329,75 @@ __device__ __forceinline__ u32x4 repack16(const float (&v)[kVec<T>])
     return (u32x4){d[0], d[1], d[2], d[3]};
 }
 
+// Values joined to (r, S, W) as differences from the largest, r = -infinity at
+// first; bad counts NaN and +infinity.
+__device__ __forceinline__ void slow_move(Stat &st, float r)       // r >= st.r
+{
+    const float d = r > st.r ? fmaxf((st.r - r) * kL2E, -1e30f) : 0.0f;
+    const float f = __builtin_amdgcn_exp2f(d);
+    st = {r, st.s * f, fmaf(st.s, d, st.w) * f};
+}
+
+template <int N>
+__device__ __forceinline__ void slow_add(Stat &st, float &bad, const float (&x)[N])
+{
+    float r = st.r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        bad += x[j] != x[j] || x[j] == INFINITY ? 1.0f : 0.0f;
+        r = fmaxf(r, x[j]);
+    }
+    if (r == -INFINITY) return;
+    slow_move(st, r);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float d = fmaxf((x[j] - r) * kL2E, -1e30f);
+        const float e = __builtin_amdgcn_exp2f(d);
+        st.s += e;
+        st.w = fmaf(e, d, st.w);
+    }
+}
+
 // (r, S, W) of a whole row by one workgroup without the products x L, for the
-// rows where those overflow or nothing is finite: values at the ends of the
-// type's range, -infinity throughout, NaN, +infinity.  r is then the row's
-// maximum, S = 0 only if it is -infinity.
+// rows where those are too coarse or nothing is finite: a maximum of 2^24 or
+// more, of either sign (masks throughout among them), -infinity throughout, NaN,
+// +infinity.  r is then the row's maximum, S = 0 only if it is -infinity.  (Four
+// such rows among 512 x 262144 bfloat16: 41 -> 68 us.)
 template <int T>
 __device__ Stat slow_stat(const LogprobArgs &a, int64_t row, Stat *part, int waves)
 {
+    typedef typename Elem<T>::type E;
+    constexpr int V = kVec<T>;
     const int tid = threadIdx.x, n = 64 * waves;
-    float r = -INFINITY, bad = 0.0f;
-    for (int64_t i = tid; i < a.n_vocab; i += n) {
-        const float x = logit<T>(a, row, i);
-        r = fmaxf(r, x);
-        bad += x != x || x == INFINITY ? 1.0f : 0.0f;
+    Stat st = {-INFINITY, 0.0f, 0.0f};
+    float bad = 0.0f;
+    // (vectors and the logits beside them as in logprob_kernel)
+    const E *x0 = (const E *)a.logits + row * a.row_stride;
+    const int len = (int)a.n_vocab;
+    const int head = min((int)((-(uintptr_t)x0 & 15) / sizeof(E)), len);
+    const int vecs = (len - head) / V, tail = len - head - vecs * V;
+    const u32x4 *xv = (const u32x4 *)(x0 + head);
+    for (int v = tid; v < vecs; v += kLoads * n) {
+        u32x4 raw[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) raw[u] = xv[min(v + u * n, vecs - 1)];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            float x[V];
+            unpack16<T>(raw[u], x);
+            if (v + u * n < vecs) slow_add(st, bad, x);
+        }
     }
+    if (tid < head + tail) {
+        const float x[1] = {(float)x0[tid < head ? tid : tid + vecs * V]};
+        slow_add(st, bad, x);
+    }
+    float r = st.r;
     for (int d = 32; d; d >>= 1) {
         r = fmaxf(r, __shfl_xor(r, d));
         bad += __shfl_xor(bad, d);
     }
-    __syncthreads();
+    __syncthreads();                                 // (`part` has been read)
     if ((tid & 63) == 0) part[tid >> 6] = {r, bad, 0.0f};
     __syncthreads();
     bad = 0.0f;
@@ -352,13 +408,7 @@ __device__ Stat slow_stat(const LogprobArgs &a, int64_t row, Stat *part, int wav
     __syncthreads();
     if (bad > 0.0f) return {r, __builtin_nanf(""), 0.0f};
     if (r == -INFINITY) return {r, 0.0f, 0.0f};
-    Stat st = {r, 0.0f, 0.0f};
-    for (int64_t i = tid; i < a.n_vocab; i += n) {
-        const float d = fmaxf((logit<T>(a, row, i) - r) * kL2E, -1e30f);
-        const float e = __builtin_amdgcn_exp2f(d);
-        st.s += e;
-        st.w = fmaf(e, d, st.w);
-    }
+    slow_move(st, r);
     for (int d = 32; d; d >>= 1) {
         st.s += __shfl_xor(st.s, d);
         st.w += __shfl_xor(st.w, d);
@@ -398,7 +448,7 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stat s
 {
     const int tid = threadIdx.x, threads = 64 * waves;
     float shift = 0.0f;                          // r L as rounded, minus r L
-    if (st.s > 0.0f && st.s < INFINITY)
+    if (st.r > kLow && st.r < -kLow && st.s > 0.0f)    // (not with a NaN)
         shift = fmaf(-st.r, kL2E, st.r * kL2E);
     else
         st = slow_stat<T>(a, row, part, waves);
