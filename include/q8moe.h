@@ -679,7 +679,8 @@ int i8_up_gate_swiglu(const void *x, int x_type, int64_t x_row_stride, const flo
  *   top_ids[t][0..n_top), top_logprobs[t][0..n_top): the n_top largest logits
  *   in descending order, ties to the lowest index, and their log probabilities
  * Everything is computed in fp32, sums of lanes and of parts of a row in trees
- * of fixed shape (results are the same bits at every call).
+ * of fixed shape (results are the same bits at every call).  Roundings leave no
+ * log probability above 0, no entropy below 0 and no lse below the largest logit.
  *   logits   [m][row_stride] of `type`, aligned to its element; row_stride in
  *            elements, >= n_vocab when m > 1 (any value: rows need no padding)
  *   tokens   int32 [m][n_given]; a token outside [0, n_vocab) gives NaN

@@ -454,10 +454,15 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stat s
         st = slow_stat<T>(a, row, part, waves);
     const bool empty = st.s == 0.0f;
     const float l2 = log2f(st.s);
-    const float lse = empty ? -INFINITY : st.r + (l2 + shift) * kLn2;
+    // (the roundings of a row with one likely token leave neither log sum exp
+    // below its logit nor the entropy below 0; NaN stays)
+    float lse = empty ? -INFINITY : st.r + (l2 + shift) * kLn2;
+    if (lse < st.r) lse = st.r;
+    float entropy = empty ? 0.0f : (l2 - st.w / st.s) * kLn2;
+    if (entropy < 0.0f) entropy = 0.0f;
     if (tid == 0) {
         if (a.lse) a.lse[row] = lse;
-        if (a.entropy) a.entropy[row] = empty ? 0.0f : (l2 - st.w / st.s) * kLn2;
+        if (a.entropy) a.entropy[row] = entropy;
     }
     auto lp = [&](float x) { return empty ? lse : x - lse; };
     for (int i = tid; i < a.n_given; i += threads) {

@@ -79,3 +79,27 @@ def test_wide_rows(q, v, t):  # noqa: F811
     tokens = np.array([[v // 2, v - 2]] * 8, np.int32)
     for n_top in (0, 7):
         _check(q, x, t, tokens, n_top)
+
+
+@pytest.mark.parametrize("t", i8_ref.TYPES)
+@pytest.mark.parametrize("v", [1, 40, 1000, 40000])
+def test_signs(q, v, t):  # noqa: F811
+    """No log probability above 0, no entropy below 0, no log sum exp below the
+    largest logit; with one visible token the entropy and its log probability
+    are next to 0."""
+    rng = synth.rng("lpsigns", str(v))
+    x = np.full((400, v), -np.inf)
+    at = rng.integers(0, v, 400)
+    x[np.arange(400), at] = rng.normal(size=400) * np.exp(rng.normal(size=400) * 2)
+    x[0, at[0]] = 0.36999786
+    x[100:200][np.isneginf(x[100:200])] = -3e4           # (0 beside the visible one)
+    # one token far above the others, and rows of a few equal tokens
+    x[200:300] = np.where(np.isneginf(x[200:300]), -20.0, 5.0 + rng.random((100, 1)))
+    x[300:] = np.where(rng.random((100, v)) < 0.5, x[300:], rng.normal(size=(100, 1)) * 7)
+    out = _check(q, x, t, at[:, None].astype(np.int32), 1)
+    top = np.max(x, axis=1)
+    import torch
+    top = torch.tensor(top).to(i8_ref.torch_type(t)).float().cuda()
+    assert bool((out.lse >= top).all())
+    assert bool((out.entropy >= 0).all())
+    assert bool((out.logprob <= 0).all()) and bool((out.top_logprobs <= 0).all())
