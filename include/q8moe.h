@@ -696,7 +696,8 @@ int i8_up_gate_swiglu(const void *x, int x_type, int64_t x_row_stride, const flo
  * tokens and logprob may be NULL when n_given is 0, the top arrays when n_top
  * is 0.  Outputs must not overlap the inputs.
  * Workspace: logprob_workspace_bytes(m, n_vocab, n_top) bytes (0 for sizes the
- * call refuses), 256-byte aligned; contents need not be initialised; not
+ * call refuses; enough for any call of up to m rows, n_vocab logits and n_top
+ * alternatives), 256-byte aligned; contents need not be initialised; not
  * shared by calls that may run concurrently.
  */
 size_t logprob_workspace_bytes(int64_t m, int64_t n_vocab, int64_t n_top);

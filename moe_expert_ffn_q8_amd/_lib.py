@@ -1101,6 +1101,8 @@ def logprob_workspace_bytes(m, n_vocab, n_top):
 
 
 def logprob_workspace(m, n_vocab, n_top, device):
+    """Workspace of logprob_rows for up to m rows (also of fewer logits and
+    alternatives)."""
     n = logprob_workspace_bytes(m, n_vocab, n_top)
     if n == 0:
         raise Q8Error("logprob_workspace_bytes", -4)
@@ -1111,7 +1113,7 @@ def logprob_rows(logits, tokens=None, n_top=0, ws=None, out=None):
     """Log probabilities of the given tokens (int32 [m] or [m][n_given]), log
     sum exp, entropy and the n_top largest logits (ties to the lowest index)
     of each row of logits, fp32 / fp16 / bf16 [m][n_vocab].  ws:
-    logprob_workspace(m, n_vocab, n_top).  Returns a LogprobOut (`out` if
+    logprob_workspace of this many rows or more.  Returns a LogprobOut (`out` if
     given)."""
     t, stride, m, n_vocab = _rows(logits, "logits", _FLOATS)
     if n_top < 0:

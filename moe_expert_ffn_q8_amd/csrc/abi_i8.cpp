@@ -132,11 +132,13 @@ static int check_logprob_sizes(int64_t m, int64_t n_vocab, int64_t n_top)
     return Q8_OK;
 }
 
+static constexpr size_t kWsLeast = 256;
+
 size_t logprob_workspace_bytes(int64_t m, int64_t n_vocab, int64_t n_top)
 {
     if (check_logprob_sizes(m, n_vocab, n_top)) return 0;
     const size_t b = q8::logprob_ws_bytes(m, n_vocab, n_top);
-    return b < 256 ? 256 : (b + 255) / 256 * 256;
+    return b < kWsLeast ? kWsLeast : (b + 255) / 256 * 256;
 }
 
 int logprob_rows(const void *logits, int type, int64_t row_stride, const int32_t *tokens,
@@ -157,7 +159,8 @@ int logprob_rows(const void *logits, int type, int64_t row_stride, const int32_t
         (n_top > 0 && (!aligned(top_ids, 4) || !aligned(top_logprobs, 4))) ||
         (lse && !aligned(lse, 4)) || (entropy && !aligned(entropy, 4)))
         return Q8_E_ALIGN;
-    if (!ws || ws_bytes < logprob_workspace_bytes(m, n_vocab, n_top)) return Q8_E_WORKSPACE;
+    if (!ws || ws_bytes < kWsLeast || ws_bytes < q8::logprob_ws_needed(m, n_vocab, n_top))
+        return Q8_E_WORKSPACE;
     if (!aligned(ws, 256)) return Q8_E_ALIGN;
     q8::LogprobArgs a;
     a.logits = logits; a.tokens = tokens; a.logprob = logprob; a.lse = lse; a.entropy = entropy;

@@ -770,11 +770,20 @@ int launch_type(const LogprobArgs &a, void *ws, hipStream_t stream)
 
 }  // namespace
 
+size_t logprob_ws_needed(int64_t m, int64_t n_vocab, int64_t n_top)
+{
+    const Cut c = cut(m, n_vocab);
+    return c.parts == 1 ? 0 : (size_t)m * c.parts * (8 * n_top + sizeof(Stat));
+}
+
+// What any call of up to m rows needs: rows are in most parts when they are
+// few, and never in more than 1024 parts together (cut).
 size_t logprob_ws_bytes(int64_t m, int64_t n_vocab, int64_t n_top)
 {
-    const Cut c = cut(m > 0 ? m : 1, n_vocab);
-    if (c.parts == 1) return 0;
-    return (size_t)m * c.parts * (8 * n_top + sizeof(Stat));
+    const int64_t parts = cut(1, n_vocab).parts;
+    if (parts == 1) return 0;
+    const int64_t all = m < 1024 / parts ? m * parts : 1024;
+    return (size_t)all * (8 * n_top + sizeof(Stat));
 }
 
 int launch_logprob(const LogprobArgs &a, void *ws, hipStream_t stream)

@@ -56,7 +56,8 @@ struct LogprobArgs {
 };
 
 constexpr int kLogprobMaxTop = 64;
-size_t logprob_ws_bytes(int64_t m, int64_t n_vocab, int64_t n_top);
+size_t logprob_ws_bytes(int64_t m, int64_t n_vocab, int64_t n_top);   // for up to m rows
+size_t logprob_ws_needed(int64_t m, int64_t n_vocab, int64_t n_top);  // by a call of m
 int launch_logprob(const LogprobArgs &a, void *ws, hipStream_t stream);
 
 }  // namespace q8
