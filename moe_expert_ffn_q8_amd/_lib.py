@@ -1079,10 +1079,11 @@ def i8_up_gate_swiglu(x, w, w_scale, x_scale=None, h=None, dtype=torch.float32, 
 
 class LogprobOut(NamedTuple):
     """Outputs of logprob_rows; top_ids and top_logprobs are None without
-    alternatives, logprob without given tokens."""
+    alternatives, logprob without given tokens.  In an `out`, lse and entropy
+    may be None where they are not wanted."""
     logprob: Optional[torch.Tensor]        # fp32 [m][n_given]
-    lse: torch.Tensor                      # fp32 [m]
-    entropy: torch.Tensor                  # fp32 [m]
+    lse: Optional[torch.Tensor]            # fp32 [m]
+    entropy: Optional[torch.Tensor]        # fp32 [m]
     top_ids: Optional[torch.Tensor]        # int32 [m][n_top]
     top_logprobs: Optional[torch.Tensor]   # fp32 [m][n_top]
 
@@ -1133,8 +1134,8 @@ def logprob_rows(logits, tokens=None, n_top=0, ws=None, out=None):
         raise ValueError("out: lacks an output that this call has")
     if n_given:
         given_p = _vector(out.logprob, m * n_given, torch.float32, "logprob")
-    lse_p = _vector(out.lse, m, torch.float32, "lse")
-    entropy_p = _vector(out.entropy, m, torch.float32, "entropy")
+    lse_p = None if out.lse is None else _vector(out.lse, m, torch.float32, "lse")
+    entropy_p = None if out.entropy is None else _vector(out.entropy, m, torch.float32, "entropy")
     if n_top:
         ids_p = _vector(out.top_ids, m * n_top, torch.int32, "top_ids")
         top_p = _vector(out.top_logprobs, m * n_top, torch.float32, "top_logprobs")
