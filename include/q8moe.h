@@ -789,6 +789,19 @@ int q8v_moe_r8_ffn(const moe_r8_ffn_desc *desc, int64_t n_tok, int64_t n_embd, i
                    q8_0_block *hq, int32_t *counts, int32_t *offsets, int32_t *pairs,
                    void *stream);
 
+/* q8v_i8_form: the kernel that i8_matmul (gated 0: n outputs) or
+ * i8_up_gate_swiglu (gated 1: n = n_ff) runs a product of these sizes on, or
+ * the status that refuses them; computed on the host, nothing is launched. */
+enum {
+    Q8V_I8_STREAM_INLINE = 0,          /* streamed weights, few token values, quantized inside */
+    Q8V_I8_STREAM = 1,                 /* streamed weights */
+    Q8V_I8_TILES_128 = 2,              /* tiles of 128 x 128 */
+    Q8V_I8_TILES_256 = 3,              /* tiles of 256 x 256, all of them whole */
+    Q8V_I8_TILES_256_SOME_HALVES = 4,  /* the last round of them as 256 x 128 */
+    Q8V_I8_TILES_256_HALVES = 5        /* all of them as 256 x 128 */
+};
+int q8v_i8_form(int64_t n, int64_t k, int64_t m, int gated);
+
 /* moe_route: the grouping of (t,u) slots by expert that the MoE kernels use:
  * counts[e] (int32 [n_expert]), offsets[e] (int32 [n_expert+1], exclusive
  * prefix of counts), pairs (int32 [n_tok*n_used]): t*n_used+u of every slot,

@@ -124,6 +124,19 @@ int i8_up_gate_swiglu(const void *x, int x_type, int64_t x_row_stride, const flo
                       h_type, h_row_stride, n_ff, k, m, true, ws, ws_bytes, stream);
 }
 
+int q8v_i8_form(int64_t n, int64_t k, int64_t m, int gated)
+{
+    if (int rc = check_i8_k(k)) return rc;
+    if (n <= 0 || m <= 0) return Q8_E_SHAPE;
+    if (n > q8::kI8MaxRows || m > q8::kI8MaxRows || n > q8::kI8MaxOutputs / m)
+        return Q8_E_UNSUPPORTED;
+    q8::I8Args a = {};
+    a.n = n; a.k = k; a.m = m;
+    if (q8::i8_inline_ok(a, gated != 0)) return Q8V_I8_STREAM_INLINE;
+    if (q8::i8_stream_ok(a, gated != 0)) return Q8V_I8_STREAM;
+    return q8::i8_gemm_form(a, gated != 0);
+}
+
 static int check_logprob_sizes(int64_t m, int64_t n_vocab, int64_t n_top)
 {
     if (m < 0 || n_vocab <= 0 || n_top < 0 || n_top > n_vocab) return Q8_E_SHAPE;

@@ -36,7 +36,7 @@
 //    contiguous run of tiles, up to 4 token tiles of one weight tile next to
 //    each other, so that an XCD's L2 serves both operands' reuse.
 //  * Large tiles where they fill the device, 128 x 128 ones elsewhere (rule and
-//    figures: launch_form).
+//    figures: plan).
 #include <type_traits>
 
 #include "i8_device.h"
@@ -395,26 +395,42 @@ TileGrid tile_grid(const I8Args &a, bool gated, int tile)
     return {(int)tn, (int)tm, (int)(tn * tm)};
 }
 
-template <int YT, bool GATED, bool STREAM>
-int launch_form(const I8Args &a, hipStream_t stream)
+// The tiles of a product: large ones (large.whole of them whole), or medium
+// ones, or none (more than a launch takes).
+struct Plan {
+    bool large;
+    TileGrid grid;
+};
+
+Plan plan(const I8Args &a, bool gated)
 {
-    TileGrid large = tile_grid(a, GATED, 256);
-    const TileGrid medium = tile_grid(a, GATED, 128);
+    TileGrid large = tile_grid(a, gated, 256);
+    const TileGrid medium = tile_grid(a, gated, 128);
     const int tiles = large.tiles_n * large.tiles_m, mtiles = medium.tiles_n * medium.tiles_m;
-    if (!mtiles) return Q8_E_UNSUPPORTED;
+    if (!mtiles) return {false, medium};
     // Rounds of the device's 256 CUs at the times of one round, in us at
     // k = 4096: 56 for 256 tiles of 256 x 256, 36 for 256 halves, 37 for 512
     // tiles of 128 x 128, 25 for 256 of them (the same ratios at other k).
     const int rest = tiles % 256;
     const int cost_large = tiles / 256 * 56 + (rest == 0 ? 0 : rest <= 128 ? 36 : 56);
     const int cost_medium = mtiles <= 256 ? 25 : (mtiles + 511) / 512 * 37;
-    if (cost_large <= cost_medium) {
-        if (rest <= 128) large.whole -= rest;
-        hipLaunchKernelGGL((i8_large_kernel<YT, GATED, STREAM>), dim3((unsigned)(2 * tiles - large.whole)),
-                           dim3(512), 0, stream, a, large);
-    } else
-        hipLaunchKernelGGL((i8_medium_kernel<YT, GATED, STREAM>), dim3((unsigned)mtiles), dim3(256), 0, stream,
-                           a, medium);
+    if (cost_large > cost_medium) return {false, medium};
+    if (rest <= 128) large.whole -= rest;
+    return {true, large};
+}
+
+template <int YT, bool GATED, bool STREAM>
+int launch_form(const I8Args &a, hipStream_t stream)
+{
+    const Plan p = plan(a, GATED);
+    const int tiles = p.grid.tiles_n * p.grid.tiles_m;
+    if (!tiles) return Q8_E_UNSUPPORTED;
+    if (p.large)
+        hipLaunchKernelGGL((i8_large_kernel<YT, GATED, STREAM>), dim3((unsigned)(2 * tiles - p.grid.whole)),
+                           dim3(512), 0, stream, a, p.grid);
+    else
+        hipLaunchKernelGGL((i8_medium_kernel<YT, GATED, STREAM>), dim3((unsigned)tiles), dim3(256), 0, stream,
+                           a, p.grid);
     return hipGetLastError() == hipSuccess ? 0 : -6;
 }
 
@@ -433,6 +449,15 @@ int launch_type(const I8Args &a, bool gated, hipStream_t stream)
 }
 
 }  // namespace
+
+int i8_gemm_form(const I8Args &a, bool gated)
+{
+    const Plan p = plan(a, gated);
+    const int tiles = p.grid.tiles_n * p.grid.tiles_m;
+    if (!p.large) return Q8V_I8_TILES_128;
+    return p.grid.whole == tiles ? Q8V_I8_TILES_256 : p.grid.whole ? Q8V_I8_TILES_256_SOME_HALVES
+                                                                   : Q8V_I8_TILES_256_HALVES;
+}
 
 int launch_i8_gemm(const I8Args &a, bool gated, hipStream_t stream)
 {

@@ -40,7 +40,8 @@ bool i8_inline_ok(const I8Args &a, bool gated);
 int launch_i8_stream(const I8Args &a, const void *xf, int xf_type, int64_t xf_stride, bool gated,
                      hipStream_t stream);
 
-// Many token rows, on tiles of both operands.
+// Many token rows, on tiles of both operands (i8_gemm_form: which, as Q8V_I8_*).
+int i8_gemm_form(const I8Args &a, bool gated);
 int launch_i8_gemm(const I8Args &a, bool gated, hipStream_t stream);
 
 // Log probabilities, already validated.
