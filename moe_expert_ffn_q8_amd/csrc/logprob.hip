@@ -349,13 +349,16 @@ __device__ __forceinline__ void slow_add(Stat &st, float &bad, const float (&x)[
     }
     if (r == -INFINITY) return;
     slow_move(st, r);
+    float s = 0.0f, w = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const float d = fmaxf((x[j] - r) * kL2E, -1e30f);
         const float e = __builtin_amdgcn_exp2f(d);
-        st.s += e;
-        st.w = fmaf(e, d, st.w);
+        s += e;
+        w = fmaf(e, d, w);
     }
+    st.s += s;
+    st.w += w;
 }
 
 // (r, S, W) of a whole row by one workgroup without the products x L, for the
@@ -557,7 +560,7 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
             stat_move(st, r);
             const float r2 = r * kL2E;
             auto terms = [&](auto with_low) {
-                Stat t = st;
+                Stat t = {r, 0.0f, 0.0f};
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
                     if (kPart * u >= left) break;
@@ -568,12 +571,17 @@ __global__ __launch_bounds__(64 * W) void logprob_kernel(const LogprobArgs a, co
             };
             // without the clamp of every term, 32 of 220 instructions, until a
             // sum says that it is needed
-            Stat t = st;
+            Stat t;
             if (!low) {
                 t = terms(std::false_type());
                 low = __ballot(t.w != t.w) != 0;
             }
-            st = low ? terms(std::true_type()) : t;
+            if (low) t = terms(std::true_type());
+            // (a turn's terms in a sum of their own: equal terms round to one
+            // side, and 1024 of them in one chain put the log sum exp of 262144
+            // logits 1.2e-5 off; now 7e-7)
+            st.s += t.s;
+            st.w += t.w;
         }
         if (TOP) {
             if (full) {
