@@ -6,10 +6,11 @@
 // over all of k: 32 v_mfma_i32_32x32x32_i8 per 128 bytes of k and wave tile, no
 // rescale between them, one rescale per output at the end.  Bound by the
 // matrix cores, and they by power on codes that are not mostly zeros: 8192^3
-// 441 us, 2.5 POPS; gated 2048 x 4096 x 2*14336 206 to 211 us, 2.3 POPS at 1.8
-// GHz; 512 x 4096 x 14336 30 us on part of the device.  With few steps the
-// start and end of each tile are most of the time: 333 x 768 x 50257 25 to 28 us,
-// of which the outputs are 10.
+// 441 us, 2.5 POPS; gated 2048 x 4096 x 2*14336 206 to 221 us, 2.2 to 2.3 POPS at
+// 1.8 GHz; 512 x 4096 x 14336 30 to 32 us on part of the device.  With few steps
+// the start and end of each tile are most of the time: 333 x 768 x 50257 25 to 29
+// us, of which the outputs are 10.  A long k with few outputs leaves CUs idle (k
+// is not split): 512 x 14336 x 4096 54 to 68 us.
 //
 // Work decomposition:
 //  * Workgroup = WN x WM waves, tile TN weight rows x TM tokens; a wave
@@ -410,7 +411,9 @@ Plan plan(const I8Args &a, bool gated)
     if (!mtiles) return {false, medium};
     // Rounds of the device's 256 CUs at the times of one round, in us at
     // k = 4096: 56 for 256 tiles of 256 x 256, 36 for 256 halves, 37 for 512
-    // tiles of 128 x 128, 25 for 256 of them (the same ratios at other k).
+    // tiles of 128 x 128, 25 for 256 of them.  (Full rounds: one that is half
+    // full is quicker, 128 tiles of 128 x 128 take 19 us at k = 4096 and 15 to 19
+    // per 4096 at k = 14336, which the rule does not know.)
     const int rest = tiles % 256;
     const int cost_large = tiles / 256 * 56 + (rest == 0 ? 0 : rest <= 128 ? 36 : 56);
     const int cost_medium = mtiles <= 256 ? 25 : (mtiles + 511) / 512 * 37;

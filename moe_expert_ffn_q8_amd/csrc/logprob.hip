@@ -16,10 +16,12 @@
 // first n_top stay.  Most 16-byte groups are dismissed by their maximum, which
 // the sums need anyway.
 //
-// Bounds: HBM for long rows without a list (512 x 262144 bfloat16 41.5 us, 6.5
-// TB/s), the vector instructions with one (7 to 8 per logit and 800 per wave for
-// a list of 20: 1021 x 50257 bfloat16 24 us, 4.3 TB/s; 20 us without the list),
-// the chain of launch, loads and joins for few rows (1 x 32000 8 us).
+// Bounds: HBM for long rows without a list (512 x 262144 bfloat16 42 us, 6.4
+// TB/s).  With one, 7 vector instructions per logit and 900 per wave for a list of
+// 20 keep the vector pipe busy half of the time; what the other half waits for
+// (the bound's barriers, exponentials, loads) was not separated (1021 x 50257
+// bfloat16 24 to 25 us, 4.2 TB/s; 21 us without the list).  For few rows the chain
+// of launch, loads and joins (1 x 32000 8 us).
 #include <type_traits>
 
 #include "i8_device.h"
