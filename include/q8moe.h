@@ -670,6 +670,149 @@ int i8_up_gate_swiglu(const void *x, int x_type, int64_t x_row_stride, const flo
                       int h_type, int64_t h_row_stride, int64_t n_ff, int64_t k, int64_t m,
                       void *ws, size_t ws_bytes, void *stream);
 
+/* i8_matmul_act -- i8_matmul with an activation and a residual in its epilogue:
+ *   y[t][j] = act(v) + residual[t][j],  v the i8_matmul value (with its bias)
+ * in fp32, act(v) rounded to fp32 before the sum, the sum rounded once to y's
+ * type.  Every output is the same bits whatever rows a call has, and with
+ * Q8_ACT_NONE and no residual those of i8_matmul.
+ *   residual  rows of y's type [m][residual_row_stride], aligned to the element,
+ *             residual_row_stride >= n when m > 1; NULL: none.  It may be y
+ *             itself with y's row stride (the stream is updated in place) and
+ *             must not overlap y otherwise.
+ * Everything else as i8_matmul; an act that is none of these: Q8_E_UNSUPPORTED. */
+typedef enum q8_act {
+    Q8_ACT_NONE = 0,
+    Q8_ACT_RELU = 1,       /* max(v, 0) */
+    Q8_ACT_RELU2 = 2,      /* max(v, 0)^2 */
+    Q8_ACT_GELU = 3,       /* v (1 + erf(v / sqrt 2)) / 2 */
+    Q8_ACT_GELU_TANH = 4,  /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    Q8_ACT_SILU = 5        /* v / (1 + exp(-v)) */
+} q8_act;
+
+int i8_matmul_act(const void *x, int x_type, int64_t x_row_stride, const float *x_scale,
+                  const int8_t *w, int64_t w_row_stride, const float *w_scale, const float *bias, int act,
+                  const void *residual, int64_t residual_row_stride, void *y, int y_type,
+                  int64_t y_row_stride, int64_t n, int64_t k, int64_t m, void *ws, size_t ws_bytes,
+                  void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the products of a token step: the embedding row of a token, the norms
+ * before and after a block with the residual stream between them, and the next
+ * token from the logits.
+ *
+ * embed_rows -- y[t] = scale * table[tokens[t]] from a table of floats or of
+ * int8 codes with a scale per row (a tied vocabulary matrix of i8_matmul):
+ *   table   table_type Q8_T_F32, Q8_T_F16, Q8_T_BF16: [n][table_row_stride],
+ *           aligned to the element, any k; Q8_T_I8: codes, 16-byte aligned,
+ *           k % 32 == 0, the stride a multiple of 16, and table_scale fp32 [n]
+ *           (else ignored).  Strides in elements, >= k when n > 1
+ *   tokens  int32 [m]; a token outside [0, n) gives a row of NaN
+ *   y       y_type (Q8_T_F32, Q8_T_F16, Q8_T_BF16) [m][y_row_stride], aligned to
+ *           the element, y_row_stride >= k when m > 1 (elements past k are not
+ *           written)
+ * q8_0_embed_rows -- the same from Q8_0 rows w [n][k/32] (r8 = 0) or from their
+ * R8 layout (r8 not 0: q8_0_repack_r8 of n rows), 16-byte aligned, k % 32 == 0.
+ * A value is (code * scale of its block or row) in fp32, times `scale` in fp32,
+ * rounded once to y's type.  m >= 0, n > 0, k > 0 (Q8_E_SHAPE); m <= 2^27,
+ * n < 2^31, k <= 2^20, strides <= 2^32 (Q8_E_UNSUPPORTED).  y must not overlap
+ * the inputs.
+ */
+int embed_rows(const void *table, int table_type, int64_t table_row_stride, const float *table_scale,
+               const int32_t *tokens, float scale, void *y, int y_type, int64_t y_row_stride, int64_t m,
+               int64_t n, int64_t k, void *stream);
+int q8_0_embed_rows(const void *w, int r8, const int32_t *tokens, float scale, void *y, int y_type,
+                    int64_t y_row_stride, int64_t m, int64_t n, int64_t k, void *stream);
+
+/* norm_rows -- y = norm(x) * weight + bias for m rows of n values:
+ *   layer 0:      norm(x) = x / sqrt(mean(x^2) + eps)
+ *   layer not 0:  norm(x) = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
+ * computed in 64 bits and rounded to fp32, then to y's type.
+ *   x        float rows [m][x_row_stride], aligned to the element
+ *   weight   fp32 [n];  bias  fp32 [n], or NULL
+ *   y        y_type Q8_T_F32, Q8_T_F16, Q8_T_BF16: rows aligned to the element;
+ *            Q8_T_I8: codes of the fp32 values by the row rule (those that
+ *            i8_quantize_rows gives for them), n % 32 == 0, 16-byte aligned, the
+ *            stride a multiple of 16, with y_scale fp32 [m] (else ignored)
+ *
+ * residual_norm_rows -- a block's output into the residual stream, and the next
+ * block's norm:
+ *   a             = x, or norm(x) * post_weight + post_bias where post_weight is
+ *                   given (post_bias may be NULL)
+ *   residual_out  = gate * a + residual_scale * residual, in 64 bits, rounded to
+ *                   fp32, then to residual_type
+ *   y             = norm(residual_out) * weight + bias, of the values as stored
+ *   residual      residual_type rows; residual_out the same type, may be
+ *                 residual itself with its stride (in place)
+ *   gate          NULL (1), or gate_type values, one row of n for all tokens
+ *                 (gate_row_stride 0) or a row per token
+ * Both norms take `layer` and `eps`.
+ * Row strides in elements, >= n when m > 1 (rows need no padding; elements past
+ * n are not written).  A row with a NaN gives a row of NaN (as codes: scale NaN
+ * and zero codes).  Except for residual_out = residual, outputs must not
+ * overlap the inputs or each other.
+ * m >= 0, n > 0 (Q8_E_SHAPE); n <= 65536, m <= 2^27, eps finite and >= 0, strides
+ * <= 2^32 (Q8_E_UNSUPPORTED).
+ */
+int norm_rows(const void *x, int x_type, int64_t x_row_stride, const float *weight, const float *bias,
+              float eps, int layer, void *y, int y_type, int64_t y_row_stride, float *y_scale, int64_t m,
+              int64_t n, void *stream);
+
+typedef struct residual_norm_desc {
+    const void *x;                       /* the block's output */
+    const void *residual;
+    void *residual_out;
+    const void *gate;                    /* or NULL */
+    const float *post_weight, *post_bias;/* or NULL */
+    const float *weight, *bias;          /* bias: or NULL */
+    void *y;
+    float *y_scale;                      /* codes */
+    int64_t x_row_stride, residual_row_stride, residual_out_row_stride, gate_row_stride, y_row_stride;
+    int x_type, residual_type, gate_type, y_type;
+    float residual_scale, eps;
+    int layer;
+} residual_norm_desc;
+
+int residual_norm_rows(const residual_norm_desc *desc, int64_t m, int64_t n, void *stream);
+
+/* sample_rows -- one token per row of logits (fp32, binary16 or bfloat16) from a
+ * given random number.  Take a row's tokens of finite logit in the order (logit
+ * descending, index ascending), with weights w_i = exp((x_i - M) / temperature),
+ * M the largest logit.  Kept is the shortest of these heads of that order:
+ *   top-k: its first top_k tokens                (all where top_k <= 0)
+ *   top-p: the shortest head whose mass reaches top_p times the mass of the top-k
+ *          head, at least one token              (all where top_p >= 1)
+ *   min-p: its tokens with w_i >= min_p, at least the largest logits
+ *                                                (all where min_p <= 0)
+ * and the token drawn is the first at which the running mass passes u times the
+ * mass of what is kept.
+ *   ids      int32 [m]: the token
+ *   logprob  fp32 [m]: log(w_i / mass of what is kept)
+ *   kept     int32 [m]: how many tokens are kept
+ *   u        fp32 [m], in [0, 1) (below: as 0; 1 and above: the last kept token
+ *            that has mass; NaN: as 0)
+ *   temperature, top_p, min_p fp32 [m], top_k int32 [m]: each may be NULL (1, off)
+ * A temperature that is not above 0: the largest logit, its lowest index, logprob
+ * 0, kept 1.  NaN as top_p or min_p: off.  A row without a finite logit: id -1,
+ * logprob -infinity, kept 0; a row with a NaN or +infinity: id -1, logprob NaN,
+ * kept 0.
+ * Weights and sums are those of 64-bit arithmetic: weights within 1.5e-14, summed
+ * as whole multiples of 2^-52 of the largest weight, or of 2^-61 to 2^-60 of the
+ * row's sum where that is more, so that results do not depend on the order of a
+ * sum.
+ *   logits   [m][row_stride], aligned to the element, row_stride >= n_vocab when
+ *            m > 1 (rows need no padding)
+ * m >= 0, n_vocab > 0 (Q8_E_SHAPE); n_vocab <= 2^24, m <= 2^23, strides <= 2^32
+ * (Q8_E_UNSUPPORTED).  Outputs must not overlap the inputs.
+ * Workspace: sample_workspace_bytes(m, n_vocab) bytes (0 for sizes the call
+ * refuses), 256-byte aligned; contents need not be initialised; not shared by
+ * calls that may run concurrently.
+ */
+size_t sample_workspace_bytes(int64_t m, int64_t n_vocab);
+
+int sample_rows(const void *logits, int type, int64_t row_stride, const float *u, const float *temperature,
+                const int32_t *top_k, const float *top_p, const float *min_p, int32_t *ids, float *logprob,
+                int32_t *kept, int64_t m, int64_t n_vocab, void *ws, size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------------------
  * logprob_rows -- log probabilities over rows of logits, as the vocabulary
  * products of this library write them (fp32), or in binary16 or bfloat16:

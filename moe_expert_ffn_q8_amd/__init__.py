@@ -17,7 +17,9 @@ from ._lib import (BLOCK_BYTES, EXPORTS, LIB_PATH, QK, MoeDownDesc, MoeUpGateDes
                    q8_0_matmul_r8_batched, make_r8_mm_desc, Q8R8MmDesc,
                    moe_r8_workspace, moe_r8_ffn_batched, moe_r8_ffn_batched_noalloc, moe_r8_fused_workspace, moe_r8_ffn_fused, MoeR8FfnDesc, q8_0_quantize_rows, q8_0_r8_bytes, q8_0_repack_r8, q8_empty, q8_read_probe, raw, status_str, version,
                    i8_quantize_rows, i8_workspace, i8_workspace_bytes, i8_matmul, i8_up_gate_swiglu,
-                   LogprobOut, logprob_outputs, logprob_workspace, logprob_workspace_bytes, logprob_rows)
+                   LogprobOut, logprob_outputs, logprob_workspace, logprob_workspace_bytes, logprob_rows,
+                   i8_matmul_act, embed_rows, q8_0_embed_rows, NormOut, norm_rows, residual_norm_rows,
+                   ResidualNormDesc, SampleOut, sample_outputs, sample_workspace, sample_workspace_bytes, sample_rows)
 
 __all__ = ["BLOCK_BYTES", "EXPORTS", "LIB_PATH", "QK", "MoeDownDesc", "MoeUpGateDesc", "Q8Error",
            "Q8MatmulDesc", "Q8MatmulF32Desc", "Q8UpGateDesc", "make_desc", "make_f32_desc",
@@ -33,4 +35,6 @@ __all__ = ["BLOCK_BYTES", "EXPORTS", "LIB_PATH", "QK", "MoeDownDesc", "MoeUpGate
            "moe_r8_workspace", "moe_r8_ffn_batched", "moe_r8_ffn_batched_noalloc", "moe_r8_fused_workspace", "moe_r8_ffn_fused", "MoeR8FfnDesc", "q8_0_quantize_rows", "q8_0_r8_bytes", "q8_0_repack_r8", "q8_empty", "q8_read_probe", "raw",
            "status_str", "version",
            "i8_quantize_rows", "i8_workspace", "i8_workspace_bytes", "i8_matmul", "i8_up_gate_swiglu",
-           "LogprobOut", "logprob_outputs", "logprob_workspace", "logprob_workspace_bytes", "logprob_rows"]
+           "LogprobOut", "logprob_outputs", "logprob_workspace", "logprob_workspace_bytes", "logprob_rows",
+           "i8_matmul_act", "embed_rows", "q8_0_embed_rows", "NormOut", "norm_rows", "residual_norm_rows",
+           "ResidualNormDesc", "SampleOut", "sample_outputs", "sample_workspace", "sample_workspace_bytes", "sample_rows"]

@@ -83,6 +83,15 @@ class Q8MatmulF32Desc(ctypes.Structure):
                 ("y_row_stride", _i64), ("y_batch_stride", _i64)]
 
 
+class ResidualNormDesc(ctypes.Structure):
+    _fields_ = [("x", _vp), ("residual", _vp), ("residual_out", _vp), ("gate", _vp),
+                ("post_weight", _vp), ("post_bias", _vp), ("weight", _vp), ("bias", _vp), ("y", _vp),
+                ("y_scale", _vp), ("x_row_stride", _i64), ("residual_row_stride", _i64),
+                ("residual_out_row_stride", _i64), ("gate_row_stride", _i64), ("y_row_stride", _i64),
+                ("x_type", _int), ("residual_type", _int), ("gate_type", _int), ("y_type", _int),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float), ("layer", _int)]
+
+
 class MoeUpGateDesc(ctypes.Structure):
     _fields_ = [("w_up_gate", _vp), ("x", _vp), ("ids", _vp), ("h", _vp), ("ws", _vp),
                 ("ws_bytes", _size)]
@@ -150,6 +159,17 @@ _SIGS = {
                          _i64, _vp, _size, _vp]),
     "i8_up_gate_swiglu": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _int, _i64, _i64,
                                  _i64, _i64, _vp, _size, _vp]),
+    "i8_matmul_act": (_int, [_vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int,
+                             _i64, _i64, _i64, _i64, _vp, _size, _vp]),
+    "embed_rows": (_int, [_vp, _int, _i64, _vp, _vp, ctypes.c_float, _vp, _int, _i64, _i64, _i64, _i64,
+                          _vp]),
+    "q8_0_embed_rows": (_int, [_vp, _int, _vp, ctypes.c_float, _vp, _int, _i64, _i64, _i64, _i64, _vp]),
+    "norm_rows": (_int, [_vp, _int, _i64, _vp, _vp, ctypes.c_float, _int, _vp, _int, _i64, _vp, _i64,
+                         _i64, _vp]),
+    "residual_norm_rows": (_int, [ctypes.POINTER(ResidualNormDesc), _i64, _i64, _vp]),
+    "sample_workspace_bytes": (_size, [_i64, _i64]),
+    "sample_rows": (_int, [_vp, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp,
+                           _size, _vp]),
     "q8v_i8_form": (_int, [_i64, _i64, _i64, _int]),
     "logprob_workspace_bytes": (_size, [_i64, _i64, _i64]),
     "logprob_rows": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
@@ -1017,7 +1037,7 @@ def i8_workspace(m, k, device):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated):
+def _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated, act=None, residual=None):
     xt, xs, m, k = _rows(x, "x", _ACTS)
     _, wst, n, wk = _rows(w, "w", _INT8)
     if wk != k:
@@ -1046,11 +1066,23 @@ def _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated):
         raise ValueError(f"{'h' if gated else 'y'}: shape {(y_rows, y_cols)}, expected {(m, n)}")
     if bias is not None:
         bias_p = _vector(bias, n, torch.float32, "bias")
-    index = _on(x, "x", w, w_scale, x_scale, bias, out, ws if ws_p else None).index
+    rs, residual_p = 0, None
+    if residual is not None:
+        rt, rs, r_rows, r_cols = _rows(residual, "residual", _FLOATS)
+        if rt != yt:
+            raise TypeError(f"residual: {residual.dtype}, expected {out.dtype} as y")
+        if r_rows != m or r_cols != n:
+            raise ValueError(f"residual: shape {(r_rows, r_cols)}, expected {(m, n)}")
+        residual_p = residual.data_ptr()
+    index = _on(x, "x", w, w_scale, x_scale, bias, out, ws if ws_p else None, residual).index
     if index != _current_device():
         with torch.cuda.device(index):
-            return _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated)
-    if gated:
+            return _i8_product(name, fn, x, w, w_scale, x_scale, bias, out, dtype, ws, gated, act,
+                               residual)
+    if act is not None:
+        rc = fn(x.data_ptr(), xt, xs, x_scale_p, w.data_ptr(), wst, w_scale_p, bias_p, act, residual_p,
+                rs, out.data_ptr(), yt, ys, n, k, m, ws_p, ws_bytes, _raw_stream(index))
+    elif gated:
         rc = fn(x.data_ptr(), xt, xs, x_scale_p, w.data_ptr(), wst, w_scale_p, out.data_ptr(), yt, ys,
                 n, k, m, ws_p, ws_bytes, _raw_stream(index))
     else:
@@ -1068,6 +1100,23 @@ def i8_matmul(x, w, w_scale, x_scale=None, bias=None, y=None, dtype=torch.float3
     y: fp32, fp16 or bf16 [m][n] (made with `dtype` if not given)."""
     return _i8_product("i8_matmul", _lib.i8_matmul, x, w, w_scale, x_scale, bias, y, dtype, ws,
                        False)
+
+
+_ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
+
+
+def i8_matmul_act(x, w, w_scale, x_scale=None, bias=None, act="none", residual=None, y=None,
+                  dtype=torch.float32, ws=None):
+    """y = act(i8_matmul(...)) + residual, with act one of "none", "relu",
+    "relu2" (its square), "gelu", "gelu_tanh", "silu"; residual: rows of y's
+    type [m][n], may be y itself (in place); the rest as for i8_matmul."""
+    code = _ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act: {act!r}, expected one of {list(_ACTIVATIONS)}")
+    if y is None and residual is not None:
+        dtype = residual.dtype
+    return _i8_product("i8_matmul_act", _lib.i8_matmul_act, x, w, w_scale, x_scale, bias, y, dtype, ws,
+                       False, code, residual)
 
 
 def i8_up_gate_swiglu(x, w, w_scale, x_scale=None, h=None, dtype=torch.float32, ws=None):
@@ -1152,6 +1201,226 @@ def logprob_rows(logits, tokens=None, n_top=0, ws=None, out=None):
                            ws_bytes, _raw_stream(index))
     if rc != 0:
         raise Q8Error("logprob_rows", rc)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Around the products of a token step: embedding rows, norms with the residual
+# stream, sampling.
+
+def _embed_out(tokens, k, y, dtype, device):
+    if tokens.dim() != 1:
+        raise ValueError(f"tokens: shape {tuple(tokens.shape)}, expected [m]")
+    m = tokens.shape[0]
+    _vector(tokens, m, torch.int32, "tokens")
+    if y is None:
+        y = torch.empty((m, k), dtype=dtype, device=device)
+    yt, ys, y_rows, y_cols = _rows(y, "y", _FLOATS)
+    if y_rows != m or y_cols != k:
+        raise ValueError(f"y: shape {(y_rows, y_cols)}, expected {(m, k)}")
+    return y, yt, ys, m
+
+
+def embed_rows(table, tokens, scale=1.0, table_scale=None, y=None, dtype=torch.float32):
+    """y[t] = scale * table[tokens[t]]: table fp32, fp16, bf16 [n][k], or int8
+    codes [n][k] with table_scale fp32 [n]; tokens int32 [m] (outside [0, n): a
+    row of NaN); y: fp32, fp16 or bf16 [m][k] (made with `dtype` if not given)."""
+    tt, ts, n, k = _rows(table, "table", _ACTS)
+    scale_p = None
+    if tt == 3:
+        if table_scale is None:
+            raise ValueError("table_scale: needed with int8 codes")
+        scale_p = _vector(table_scale, n, torch.float32, "table_scale")
+    elif table_scale is not None:
+        raise ValueError("table_scale: given with a table that is not int8 codes")
+    y, yt, ys, m = _embed_out(tokens, k, y, dtype, table.device)
+    index = _on(table, "table", table_scale, tokens, y).index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return embed_rows(table, tokens, scale, table_scale, y)
+    rc = _lib.embed_rows(table.data_ptr(), tt, ts, scale_p, tokens.data_ptr(), scale, y.data_ptr(), yt,
+                         ys, m, n, k, _raw_stream(index))
+    if rc != 0:
+        raise Q8Error("embed_rows", rc)
+    return y
+
+
+def q8_0_embed_rows(w, tokens, n, k, scale=1.0, r8=False, y=None, dtype=torch.float32):
+    """y[t] = scale * row tokens[t] of n Q8_0 rows of k values, or of their R8
+    layout (r8); tokens and y as for embed_rows."""
+    if n > 0 and k > 0:
+        _fit(w, q8_0_r8_bytes(n, k) if r8 else n * (k // QK) * BLOCK_BYTES, "w")
+    y, yt, ys, m = _embed_out(tokens, k, y, dtype, w.device)
+    index = _on(w, "w", tokens, y).index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return q8_0_embed_rows(w, tokens, n, k, scale, r8, y)
+    rc = _lib.q8_0_embed_rows(w.data_ptr(), bool(r8), tokens.data_ptr(), scale, y.data_ptr(), yt, ys, m,
+                              n, k, _raw_stream(index))
+    if rc != 0:
+        raise Q8Error("q8_0_embed_rows", rc)
+    return y
+
+
+class NormOut(NamedTuple):
+    """Outputs of norm_rows and residual_norm_rows."""
+    y: torch.Tensor                        # float rows, or int8 codes
+    y_scale: Optional[torch.Tensor]        # fp32 [m], of codes
+    residual: Optional[torch.Tensor]       # the updated stream
+
+
+def _norm_out(x, y, y_scale, dtype, m, n):
+    if y is None:
+        y = torch.empty((m, n), dtype=dtype, device=x.device)
+    yt, ys, y_rows, y_cols = _rows(y, "y", _ACTS)
+    if y_rows != m or y_cols != n:
+        raise ValueError(f"y: shape {(y_rows, y_cols)}, expected {(m, n)}")
+    if yt == 3:
+        if y_scale is None:
+            y_scale = torch.empty(m, dtype=torch.float32, device=x.device)
+        return y, yt, ys, y_scale, _vector(y_scale, m, torch.float32, "y_scale")
+    if y_scale is not None:
+        raise ValueError("y_scale: given with a y that is not int8 codes")
+    return y, yt, ys, None, None
+
+
+def norm_rows(x, weight, bias=None, eps=1e-5, layer=False, y=None, y_scale=None, dtype=torch.float32):
+    """y = norm(x) * weight (+ bias) of rows x, fp32 / fp16 / bf16 [m][n]: the root
+    mean square norm, or with mean and variance (layer).  weight, bias: fp32
+    [n].  y: fp32, fp16, bf16, or int8 codes with y_scale fp32 [m] (made with
+    `dtype` if not given).  Returns a NormOut."""
+    xt, xs, m, n = _rows(x, "x", _FLOATS)
+    weight_p = _vector(weight, n, torch.float32, "weight")
+    bias_p = None if bias is None else _vector(bias, n, torch.float32, "bias")
+    y, yt, ys, y_scale, scale_p = _norm_out(x, y, y_scale, dtype, m, n)
+    index = _on(x, "x", weight, bias, y, y_scale).index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return norm_rows(x, weight, bias, eps, layer, y, y_scale)
+    rc = _lib.norm_rows(x.data_ptr(), xt, xs, weight_p, bias_p, eps, layer, y.data_ptr(), yt, ys, scale_p,
+                        m, n, _raw_stream(index))
+    if rc != 0:
+        raise Q8Error("norm_rows", rc)
+    return NormOut(y, y_scale, None)
+
+
+def residual_norm_rows(x, residual, weight, bias=None, post_weight=None, post_bias=None, gate=None,
+                       residual_scale=1.0, eps=1e-5, layer=False, residual_out=None, y=None,
+                       y_scale=None, dtype=torch.float32):
+    """A block's output x into the residual stream, and the next norm:
+    residual_out = gate * x + residual_scale * residual (x normed with
+    post_weight and post_bias first, if given), y = norm(residual_out) * weight
+    (+ bias).  x, residual: float rows [m][n], each of its own type;
+    residual_out: of residual's type, may be residual itself; gate: float [n] or
+    [m][n]; the rest as for norm_rows.  Returns a NormOut."""
+    d = ResidualNormDesc()
+    d.x_type, d.x_row_stride, m, n = _rows(x, "x", _FLOATS)
+    d.x = x.data_ptr()
+    if residual_out is None:
+        residual_out = torch.empty((m, n), dtype=residual.dtype, device=x.device)
+    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
+        rt, rs, rows, cols = _rows(t, name, _FLOATS)
+        if rows != m or cols != n:
+            raise ValueError(f"{name}: shape {(rows, cols)}, expected {(m, n)}")
+        if t is residual:
+            d.residual_type, d.residual_row_stride = rt, rs
+        elif rt != d.residual_type:
+            raise TypeError(f"residual_out: {t.dtype}, expected {residual.dtype} as residual")
+        else:
+            d.residual_out_row_stride = rs
+    if residual_out is residual:
+        d.residual_out_row_stride = d.residual_row_stride
+    d.residual, d.residual_out = residual.data_ptr(), residual_out.data_ptr()
+    if gate is not None:
+        if gate.dim() == 1:
+            d.gate_type = _FLOATS.get(gate.dtype, -1)
+            if d.gate_type < 0:
+                raise TypeError(f"gate: {gate.dtype}, expected a float type")
+            d.gate = _vector(gate, n, gate.dtype, "gate")
+        else:
+            d.gate_type, d.gate_row_stride, rows, cols = _rows(gate, "gate", _FLOATS)
+            if rows != m or cols != n:
+                raise ValueError(f"gate: shape {(rows, cols)}, expected {(n,)} or {(m, n)}")
+            d.gate = gate.data_ptr()
+    if post_weight is not None:
+        d.post_weight = _vector(post_weight, n, torch.float32, "post_weight")
+    if post_bias is not None:
+        if post_weight is None:
+            raise ValueError("post_bias: given without post_weight")
+        d.post_bias = _vector(post_bias, n, torch.float32, "post_bias")
+    d.weight = _vector(weight, n, torch.float32, "weight")
+    if bias is not None:
+        d.bias = _vector(bias, n, torch.float32, "bias")
+    y, d.y_type, d.y_row_stride, y_scale, d.y_scale = _norm_out(x, y, y_scale, dtype, m, n)
+    d.y = y.data_ptr()
+    d.residual_scale, d.eps, d.layer = residual_scale, eps, layer
+    index = _on(x, "x", residual, residual_out, gate, post_weight, post_bias, weight, bias, y,
+                y_scale).index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return residual_norm_rows(x, residual, weight, bias, post_weight, post_bias, gate,
+                                      residual_scale, eps, layer, residual_out, y, y_scale)
+    rc = _lib.residual_norm_rows(d, m, n, _raw_stream(index))
+    if rc != 0:
+        raise Q8Error("residual_norm_rows", rc)
+    return NormOut(y, y_scale, residual_out)
+
+
+class SampleOut(NamedTuple):
+    """Outputs of sample_rows."""
+    ids: torch.Tensor                      # int32 [m], -1 for a row that is no distribution
+    logprob: torch.Tensor                  # fp32 [m], of the token among what is kept
+    kept: torch.Tensor                     # int32 [m]
+
+
+def sample_outputs(m, device):
+    """Output tensors for sample_rows (its `out`)."""
+    return SampleOut(torch.empty(m, dtype=torch.int32, device=device),
+                     torch.empty(m, dtype=torch.float32, device=device),
+                     torch.empty(m, dtype=torch.int32, device=device))
+
+
+def sample_workspace_bytes(m, n_vocab):
+    return int(_lib.sample_workspace_bytes(m, n_vocab))
+
+
+def sample_workspace(m, n_vocab, device):
+    """Workspace of sample_rows for up to m rows of up to n_vocab logits."""
+    n = sample_workspace_bytes(m, n_vocab)
+    if n == 0:
+        raise Q8Error("sample_workspace_bytes", -4)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def sample_rows(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, ws=None, out=None):
+    """A token per row of logits, fp32 / fp16 / bf16 [m][n_vocab], from random
+    numbers u fp32 [m] in [0, 1), after temperature, top-k, top-p and min-p
+    (fp32 [m], top_k int32 [m], each may be None; temperature 0: the largest
+    logit).  ws: sample_workspace of this many rows and logits or more.
+    Returns a SampleOut (`out` if given)."""
+    t, stride, m, n_vocab = _rows(logits, "logits", _FLOATS)
+    u_p = _vector(u, m, torch.float32, "u")
+    temp_p = None if temperature is None else _vector(temperature, m, torch.float32, "temperature")
+    k_p = None if top_k is None else _vector(top_k, m, torch.int32, "top_k")
+    p_p = None if top_p is None else _vector(top_p, m, torch.float32, "top_p")
+    min_pp = None if min_p is None else _vector(min_p, m, torch.float32, "min_p")
+    if out is None:
+        out = sample_outputs(m, logits.device)
+    ids_p = _vector(out.ids, m, torch.int32, "ids")
+    logprob_p = _vector(out.logprob, m, torch.float32, "logprob")
+    kept_p = _vector(out.kept, m, torch.int32, "kept")
+    ws_p, ws_bytes = None, 0
+    if ws is not None:
+        ws_bytes = ws.numel()
+        ws_p = _vector(ws, ws_bytes, torch.uint8, "ws")
+    index = _on(logits, "logits", u, temperature, top_k, top_p, min_p, ws, *out).index
+    if index != _current_device():
+        with torch.cuda.device(index):
+            return sample_rows(logits, u, temperature, top_k, top_p, min_p, ws, out)
+    rc = _lib.sample_rows(logits.data_ptr(), t, stride, u_p, temp_p, k_p, p_p, min_pp, ids_p, logprob_p,
+                          kept_p, m, n_vocab, ws_p, ws_bytes, _raw_stream(index))
+    if rc != 0:
+        raise Q8Error("sample_rows", rc)
     return out
 
 

@@ -35,10 +35,16 @@ int check_rows(const void *p, int64_t &stride, int64_t rows, int64_t k, int64_t 
     return stride > q8::kI8MaxRowBytes / bytes ? Q8_E_UNSUPPORTED : Q8_OK;
 }
 
+struct Epilogue {
+    int act;
+    const void *residual;
+    int64_t r_stride;
+};
+
 int i8_product(const void *x, int x_type, int64_t x_row_stride, const float *x_scale,
                const int8_t *w, int64_t w_row_stride, const float *w_scale, const float *bias,
                void *y, int y_type, int64_t y_row_stride, int64_t n, int64_t k, int64_t m,
-               bool gated, void *ws, size_t ws_bytes, void *stream)
+               bool gated, void *ws, size_t ws_bytes, void *stream, const Epilogue *epi = nullptr)
 {
     if (int rc = check_i8_k(k)) return rc;
     if (n < 0 || m < 0) return Q8_E_SHAPE;
@@ -57,7 +63,17 @@ int i8_product(const void *x, int x_type, int64_t x_row_stride, const float *x_s
         (bias && !aligned(bias, 4)))
         return Q8_E_ALIGN;
     const hipStream_t st = (hipStream_t)stream;
-    q8::I8Args a;
+    q8::I8Args a = {};
+    if (epi) {
+        if (epi->residual) {
+            if (!aligned(epi->residual, type_bytes(y_type))) return Q8_E_ALIGN;
+            a.r_stride = m == 1 ? n : epi->r_stride;
+            if (a.r_stride < n) return Q8_E_SHAPE;
+        }
+        a.epilogue = true;
+        a.act = epi->act;
+        a.residual = epi->residual;
+    }
     a.w = w; a.w_scale = w_scale; a.bias = bias; a.y = y;
     a.w_stride = w_row_stride; a.y_stride = y_row_stride;
     a.n = n; a.k = k; a.m = m; a.y_type = y_type;
@@ -122,6 +138,18 @@ int i8_up_gate_swiglu(const void *x, int x_type, int64_t x_row_stride, const flo
 {
     return i8_product(x, x_type, x_row_stride, x_scale, w, w_row_stride, w_scale, nullptr, h,
                       h_type, h_row_stride, n_ff, k, m, true, ws, ws_bytes, stream);
+}
+
+int i8_matmul_act(const void *x, int x_type, int64_t x_row_stride, const float *x_scale,
+                  const int8_t *w, int64_t w_row_stride, const float *w_scale, const float *bias, int act,
+                  const void *residual, int64_t residual_row_stride, void *y, int y_type,
+                  int64_t y_row_stride, int64_t n, int64_t k, int64_t m, void *ws, size_t ws_bytes,
+                  void *stream)
+{
+    if (act < Q8_ACT_NONE || act > Q8_ACT_SILU) return Q8_E_UNSUPPORTED;
+    const Epilogue e = {act, residual, residual_row_stride};
+    return i8_product(x, x_type, x_row_stride, x_scale, w, w_row_stride, w_scale, bias, y, y_type,
+                      y_row_stride, n, k, m, false, ws, ws_bytes, stream, &e);
 }
 
 int q8v_i8_form(int64_t n, int64_t k, int64_t m, int gated)

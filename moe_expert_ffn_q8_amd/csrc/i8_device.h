@@ -99,7 +99,7 @@ __device__ __forceinline__ float i8_rescale(int sum, float sx, float sw, float b
 // silu(g) * u = g / (1 + exp(-g)) * u.  exp(-g) as 2^t with t = -g*log2(e) and
 // the rounding error r of t put back as a factor 1 + r*ln 2 (t alone would cost
 // |t| * 2^-24 relative); the clamp keeps infinities of g from making NaN there.
-__device__ __forceinline__ float silu_mul(float g, float u)
+__device__ __forceinline__ float one_plus_exp_neg(float g)
 {
     const float c = fminf(fmaxf(-g, -104.0f), 104.0f);
     constexpr float kL2E = 1.44269504088896341f, kL2ELo = 1.925963033500e-8f;
@@ -107,8 +107,43 @@ __device__ __forceinline__ float silu_mul(float g, float u)
     const float r = fmaf(c, kL2E, -t) + c * kL2ELo;
     const float e0 = __builtin_amdgcn_exp2f(t);
     const float e = fmaf(e0, r * 0.693147180559945f, e0);
-    const float d = 1.0f + (e0 < 3.0e38f ? e : e0);
-    return g * __builtin_amdgcn_rcpf(d) * u;
+    return 1.0f + (e0 < 3.0e38f ? e : e0);
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    return g * __builtin_amdgcn_rcpf(one_plus_exp_neg(g)) * u;
+}
+
+// The activations of q8_act (the value pinned as fp32: a last product merged with
+// the residual's sum would round once where another kernel rounds twice).
+// gelu(v) = v / 2 erfc(-v / sqrt 2) keeps its small
+// values on the left; the tanh form is v / (1 + exp(-s)) with
+// s = sqrt(8 / pi) (v + 0.044715 v^3).
+__device__ __forceinline__ float activate_value(int act, float v)
+{
+    switch (act) {
+    case Q8_ACT_RELU: return v < 0.0f ? 0.0f : v;
+    case Q8_ACT_RELU2: {
+        const float r = v < 0.0f ? 0.0f : v;
+        return r * r;
+    }
+    case Q8_ACT_GELU: return 0.5f * v * erfcf(v * -0.707106781186547524f);
+    case Q8_ACT_GELU_TANH: {
+        constexpr float c = 1.59576912160573071f;       // sqrt(8 / pi)
+        const float s = v * fmaf(v * v, c * 0.044715f, c);
+        return v * __builtin_amdgcn_rcpf(one_plus_exp_neg(s));
+    }
+    case Q8_ACT_SILU: return silu_mul(v, 1.0f);
+    default: return v;
+    }
+}
+
+__device__ __forceinline__ float activate(int act, float v)
+{
+    v = activate_value(act, v);
+    asm("" : "+v"(v));
+    return v;
 }
 
 // A value rounded to nearest even to the output's type.  (It is pinned as fp32
@@ -125,6 +160,14 @@ template <int T>
 __device__ __forceinline__ void store_out(void *y, int64_t i, float v)
 {
     ((typename Elem<T>::type *)y)[i] = round_out<T>(v);
+}
+
+// The value at an element of a float type.
+__device__ __forceinline__ float load_in(const void *x, int type, int64_t i)
+{
+    return type == Q8_T_F32   ? ((const float *)x)[i]
+           : type == Q8_T_F16 ? (float)((const _Float16 *)x)[i]
+                              : (float)((const __bf16 *)x)[i];
 }
 
 // Two values of a 16-bit type in a dword (one instruction for both).
@@ -166,6 +209,37 @@ __device__ __forceinline__ void store16(uint8_t *y, u32x4 v, int left)
             else
                 ((uint16_t *)y)[r] = (uint16_t)(d[r / 2] >> (16 * (r & 1)));
         }
+}
+
+// 16 bytes of outputs from their fp32 values.
+template <int T>
+__device__ __forceinline__ u32x4 pack_vec(const float (&v)[kVec<T>])
+{
+    if constexpr (T == Q8_T_F32)
+        return (u32x4){__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
+                       __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])};
+    else
+        return (u32x4){pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
+}
+
+// 16 bytes of elements, the first `left` of them (element alignment is enough;
+// 0 beyond).
+template <int T>
+__device__ __forceinline__ u32x4 load16(const uint8_t *p, int left)
+{
+    typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+    constexpr int V = kVec<T>;
+    if (left >= V) return *(const u32x4_any *)p;
+    uint32_t d[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int r = 0; r < V - 1; ++r)
+        if (r < left) {
+            if constexpr (T == Q8_T_F32)
+                d[r] = ((const uint32_t *)p)[r];
+            else
+                d[r / 2] |= (uint32_t)((const uint16_t *)p)[r] << (16 * (r & 1));
+        }
+    return (u32x4){d[0], d[1], d[2], d[3]};
 }
 
 // Up to 4 consecutive values.

@@ -56,8 +56,9 @@ constexpr int kOut = 0x7ff00000;  // an offset past every resource: reads zero
 
 // One tile: outputs n0 .. (TN of them, TN/2 gated), tokens m0 .. m0 + TM - 1.
 // w0 .. x1: the stages, separate LDS objects, so that a fragment read waits for
-// its own stage's loads only.  STREAM: outputs are written past the caches.
-template <int TN, int TM, int WN, int WM, int YT, bool GATED, bool STREAM>
+// its own stage's loads only.  STREAM: outputs are written past the caches.  EPI:
+// y = act(value) + residual.
+template <int TN, int TM, int WN, int WM, int YT, bool GATED, bool STREAM, bool EPI>
 __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0, uint8_t *w0,
                                         uint8_t *w1, uint8_t *w2, uint8_t *x0, uint8_t *x1)
 {
@@ -316,7 +317,66 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
             }
         }
     };
-    if (!GATED && a.bias)
+    if constexpr (EPI) {
+        // fp32 values through LDS 32 columns at a time: the residual is added, and
+        // the sum rounded, where a lane holds 16 bytes of outputs
+        constexpr int V = 16 / kES, kRow = 32 / V, kTurns = 32 * kRow / 64;   // 16-byte pieces a row
+        const int e_row = lane / kRow, e_col = lane % kRow * V;
+        const int e_rows = x_rows - wm * MI * 32 - e_row, e_cols = w_rows - wn * kWaveCols - e_col;
+        uint8_t *ye = (uint8_t *)a.y + (m0 + wm * MI * 32 + e_row) * y_bytes + (n0 + wn * kWaveCols + e_col) * kES;
+        const int64_t r_bytes = a.r_stride * kES;
+        const uint8_t *re = (const uint8_t *)a.residual + (m0 + wm * MI * 32 + e_row) * r_bytes +
+                            (n0 + wn * kWaveCols + e_col) * kES;
+#pragma unroll
+        for (int j = 0; j < MI; ++j) {
+#pragma unroll
+            for (int i = 0; i < kOutTiles; ++i) {
+                u32x4 res[kTurns];
+#pragma unroll
+                for (int e = 0; e < kTurns; ++e) {
+                    const int up = e * (64 / kRow);
+                    res[e] = (u32x4){0u, 0u, 0u, 0u};
+                    if (a.residual && 32 * j + up < e_rows && 32 * i < e_cols)
+                        res[e] = load16<YT>(re + (32 * j + up) * r_bytes + 32 * i * kES, e_cols - 32 * i);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int row = (wn * NI + i) * 32 + 8 * q + 4 * h;
+                    const float4 sg = *(const float4 *)(scales + row), sb = *(const float4 *)(scales + TN + row);
+                    const float g4[4] = {sg.x, sg.y, sg.z, sg.w}, b4[4] = {sb.x, sb.y, sb.z, sb.w};
+                    float v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int s = acc[i][j][4 * q + r];
+                        v[r] = activate(a.act, a.bias ? i8_rescale(s, s_x[j], g4[r], b4[r])
+                                                      : i8_rescale(s, s_x[j], g4[r]));
+                    }
+                    *(float4 *)(turn + li * 128 + 16 * ((2 * q + h) ^ ((li >> 1) & 7))) =
+                        make_float4(v[0], v[1], v[2], v[3]);
+                }
+                wave_lds_sync();
+#pragma unroll
+                for (int e = 0; e < kTurns; ++e) {
+                    const int up = e * (64 / kRow), row = up + e_row;
+                    float v[V], r[V];
+#pragma unroll
+                    for (int c = 0; c < V / 4; ++c) {
+                        const float4 o = *(const float4 *)(turn + row * 128 + 16 * ((e_col / 4 + c) ^ ((row >> 1) & 7)));
+                        v[4 * c] = o.x; v[4 * c + 1] = o.y; v[4 * c + 2] = o.z; v[4 * c + 3] = o.w;
+                    }
+                    if (a.residual) {
+                        unpack16<YT>(res[e], r);
+#pragma unroll
+                        for (int c = 0; c < V; ++c) v[c] += r[c];
+                    }
+                    if (32 * j + up < e_rows && 32 * i < e_cols)
+                        store16<YT, STREAM>(ye + (32 * j + up) * y_bytes + 32 * i * kES, pack_vec<YT>(v),
+                                            e_cols - 32 * i);
+                }
+                wave_lds_sync();
+            }
+        }
+    } else if (!GATED && a.bias)
         outputs(std::integral_constant<bool, !GATED>());
     else
         outputs(std::integral_constant<bool, false>());
@@ -348,7 +408,7 @@ __device__ __forceinline__ int xcd_run(int b, int n)
 // 256 x 256, one workgroup of 8 waves per CU: 2.5 POPS where all CUs have work.
 // The last tiles, where they would occupy half of the CUs or fewer, are
 // computed as halves of 128 tokens, on twice as many CUs.
-template <int YT, bool GATED, bool STREAM>
+template <int YT, bool GATED, bool STREAM, bool EPI>
 __global__ __launch_bounds__(512, 2) void i8_large_kernel(const I8Args a, const TileGrid g)
 {
     __shared__ __align__(16) uint8_t w0[256 * kStep];
@@ -361,19 +421,19 @@ __global__ __launch_bounds__(512, 2) void i8_large_kernel(const I8Args a, const 
     int tn, tm;
     if (b < g.whole) {
         g.at(xcd_run(b, g.whole), tn, tm);
-        i8_tile<256, 256, 4, 2, YT, GATED, STREAM>(a, (int64_t)tn * kCols, (int64_t)tm * 256, w0, w1,
-                                                   w2, x0, x1);
+        i8_tile<256, 256, 4, 2, YT, GATED, STREAM, EPI>(a, (int64_t)tn * kCols, (int64_t)tm * 256, w0,
+                                                        w1, w2, x0, x1);
     } else {
         const int half = xcd_run(b - g.whole, 2 * (g.tiles_n * g.tiles_m - g.whole));
         g.at(g.whole + half / 2, tn, tm);
         const int64_t m0 = (int64_t)tm * 256 + 128 * (half & 1);
         if (m0 < a.m)
-            i8_tile<256, 128, 4, 2, YT, GATED, STREAM>(a, (int64_t)tn * kCols, m0, w0, w1, w2, x0, x1);
+            i8_tile<256, 128, 4, 2, YT, GATED, STREAM, EPI>(a, (int64_t)tn * kCols, m0, w0, w1, w2, x0, x1);
     }
 }
 
 // 128 x 128, two workgroups of 4 waves per CU.
-template <int YT, bool GATED, bool STREAM>
+template <int YT, bool GATED, bool STREAM, bool EPI>
 __global__ __launch_bounds__(256, 2) void i8_medium_kernel(const I8Args a, const TileGrid g)
 {
     __shared__ __align__(16) uint8_t w0[128 * kStep];
@@ -383,7 +443,7 @@ __global__ __launch_bounds__(256, 2) void i8_medium_kernel(const I8Args a, const
     __shared__ __align__(16) uint8_t x1[128 * kStep];
     int tn, tm;
     g.at(xcd_run(blockIdx.x, g.tiles_n * g.tiles_m), tn, tm);
-    i8_tile<128, 128, 2, 2, YT, GATED, STREAM>(a, (int64_t)tn * (GATED ? 64 : 128), (int64_t)tm * 128,
+    i8_tile<128, 128, 2, 2, YT, GATED, STREAM, EPI>(a, (int64_t)tn * (GATED ? 64 : 128), (int64_t)tm * 128,
                                                w0, w1, w2, x0, x1);
 }
 
@@ -422,17 +482,17 @@ Plan plan(const I8Args &a, bool gated)
     return {true, large};
 }
 
-template <int YT, bool GATED, bool STREAM>
+template <int YT, bool GATED, bool STREAM, bool EPI>
 int launch_form(const I8Args &a, hipStream_t stream)
 {
     const Plan p = plan(a, GATED);
     const int tiles = p.grid.tiles_n * p.grid.tiles_m;
     if (!tiles) return Q8_E_UNSUPPORTED;
     if (p.large)
-        hipLaunchKernelGGL((i8_large_kernel<YT, GATED, STREAM>), dim3((unsigned)(2 * tiles - p.grid.whole)),
+        hipLaunchKernelGGL((i8_large_kernel<YT, GATED, STREAM, EPI>), dim3((unsigned)(2 * tiles - p.grid.whole)),
                            dim3(512), 0, stream, a, p.grid);
     else
-        hipLaunchKernelGGL((i8_medium_kernel<YT, GATED, STREAM>), dim3((unsigned)tiles), dim3(256), 0, stream,
+        hipLaunchKernelGGL((i8_medium_kernel<YT, GATED, STREAM, EPI>), dim3((unsigned)tiles), dim3(256), 0, stream,
                            a, p.grid);
     return hipGetLastError() == hipSuccess ? 0 : -6;
 }
@@ -447,8 +507,12 @@ int launch_type(const I8Args &a, bool gated, hipStream_t stream)
 {
     if constexpr (YT != Q8_T_F32)
         if (a.y_stride * 2 % 128 == 0 && (uintptr_t)a.y % 128 == 0)
-            return gated ? launch_form<YT, true, true>(a, stream) : launch_form<YT, false, true>(a, stream);
-    return gated ? launch_form<YT, true, false>(a, stream) : launch_form<YT, false, false>(a, stream);
+            return gated        ? launch_form<YT, true, true, false>(a, stream)
+                   : a.epilogue ? launch_form<YT, false, true, true>(a, stream)
+                                : launch_form<YT, false, true, false>(a, stream);
+    return gated        ? launch_form<YT, true, false, false>(a, stream)
+           : a.epilogue ? launch_form<YT, false, false, true>(a, stream)
+                        : launch_form<YT, false, false, false>(a, stream);
 }
 
 }  // namespace

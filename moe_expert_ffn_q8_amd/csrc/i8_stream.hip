@@ -145,8 +145,9 @@ struct Rows<-1, kWaves, kValues> {
 
 // NI: 16-row weight tiles (in the gated form NI/2 of gate rows, then NI/2 of
 // the up rows of the same outputs).  MT: 16-token tiles.
-// XT: the type of token rows taken as given (XL), or -1.
-template <int NI, int MT, int kWaves, int XT, bool GATED>
+// XT: the type of token rows taken as given (XL), or -1.  EPI: y = act(value) +
+// residual.
+template <int NI, int MT, int kWaves, int XT, bool GATED, bool EPI>
 __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs p)
 {
     constexpr bool XL = XT >= 0;
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
     constexpr int kTiles = NI * MT;
     constexpr int kDone = GATED ? kTiles / 2 : kTiles;
     constexpr int kMine = (kDone + kWaves - 1) / kWaves;
-    float s_gate[kMine][4], s_up[kMine][4], s_x[kMine], bias[kMine][4];
+    float s_gate[kMine][4], s_up[kMine][4], s_x[kMine], bias[kMine][4], res[kMine][4];
 #pragma unroll
     for (int o = 0; o < kMine; ++o) {
         const int tile = min(o * kWaves + wave, kDone - 1);
@@ -261,6 +262,7 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
             s_gate[o][r] = a.w_scale[n];
             s_up[o][r] = GATED ? a.w_scale[a.n + n] : 0.0f;
             bias[o][r] = !GATED && a.bias ? a.bias[n] : 0.0f;
+            if (EPI) res[o][r] = a.residual ? load_in(a.residual, a.y_type, t * a.r_stride + n) : 0.0f;
         }
     }
     const int per = k * (XT == Q8_T_F32 ? 4 : XT == Q8_T_I8 ? 1 : 2) / 16;
@@ -312,6 +314,10 @@ __global__ __launch_bounds__(64 * kWaves) void i8_stream_kernel(const StreamArgs
             else
                 v[r] = a.bias ? i8_rescale(s[r], sx, s_gate[o][r], bias[o][r])
                               : i8_rescale(s[r], sx, s_gate[o][r]);
+            if (EPI) {
+                v[r] = activate(a.act, v[r]);
+                if (a.residual) v[r] += res[o][r];
+            }
         }
         const int64_t n = n0 + 16 * i + 4 * grp, at = (m0 + tr) * a.y_stride + n;
         const int left = (int)min((int64_t)4, a.n - n);
@@ -339,11 +345,13 @@ int launch(const StreamArgs &p, bool gated, hipStream_t stream)
     bool done = false;
     if constexpr (NI > 1)            // (shape() gives the gated form two rows of tiles)
         if (gated) {
-            hipLaunchKernelGGL((i8_stream_kernel<NI, MT, NW, XT, true>), grid, dim3(64 * NW), 0, stream, p);
+            hipLaunchKernelGGL((i8_stream_kernel<NI, MT, NW, XT, true, false>), grid, dim3(64 * NW), 0, stream, p);
             done = true;
         }
-    if (!done)
-        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, NW, XT, false>), grid, dim3(64 * NW), 0, stream, p);
+    if (!done && p.a.epilogue)
+        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, NW, XT, false, true>), grid, dim3(64 * NW), 0, stream, p);
+    else if (!done)
+        hipLaunchKernelGGL((i8_stream_kernel<NI, MT, NW, XT, false, false>), grid, dim3(64 * NW), 0, stream, p);
     return hipGetLastError() == hipSuccess ? 0 : -6;
 }
 

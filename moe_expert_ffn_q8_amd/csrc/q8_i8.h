@@ -26,6 +26,11 @@ struct I8Args {
     int64_t y_stride;             // elements
     int64_t n, k, m;              // n: output columns (n_ff in the gated form)
     int y_type;                   // Q8_T_F32, Q8_T_F16, Q8_T_BF16
+    // y = act(value) + residual, where `epilogue` is set (not in the gated form)
+    bool epilogue;
+    int act;                      // q8_act
+    const void *residual;         // of y's type, or null
+    int64_t r_stride;             // elements
 };
 
 // Rows of k values of `type` to codes and scales.
