@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "i8_device.h"
+#include "order_device.h"
 #include "q8_i8.h"
 
 namespace q8 {
@@ -108,59 +109,11 @@ __device__ __forceinline__ Stat wave_join(Stat st)
     return {st.r, wave_reduce<false>(st.s), wave_reduce<false>(st.w)};
 }
 
-// Order of the top list: larger value first, then lower index; NaN last.  No
-// key of a logit is 0.
-__device__ __forceinline__ uint32_t value_key(float x)
-{
-    const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);       // -0 -> +0
-    const uint32_t key = (u >> 31) ? ~u : (u | 0x80000000u);
-    return x != x ? 0u : key;
-}
-
-__device__ __forceinline__ uint64_t order_key(float x, uint32_t i)
-{
-    return ((uint64_t)value_key(x) << 32) | (uint32_t)~i;
-}
-
-__device__ __forceinline__ float key_value(uint64_t key)
-{
-    const uint32_t k = (uint32_t)(key >> 32);
-    if (k == 0) return __builtin_nanf("");
-    return __builtin_bit_cast(float, (k >> 31) ? (k & 0x7fffffffu) : ~k);
-}
-
-__device__ __forceinline__ int key_index(uint64_t key) { return (int)~(uint32_t)key; }
-
 // Moves within rows of 16 lanes.
 template <int Ctrl>
 __device__ __forceinline__ uint32_t row_move(uint32_t v)
 {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, Ctrl, 0xf, 0xf, false);
-}
-
-// The n-th largest of 64 keys, one per lane, its low half cut (0: fewer than n
-// keys are not 0).
-__device__ __forceinline__ uint32_t nth_key(uint32_t key, int n)
-{
-    uint32_t t = 0;
-    for (int b = 31; b >= 16; --b) {
-        const uint32_t c = t | (1u << b);
-        if (__popcll(__ballot(key >= c)) >= n) t = c;
-    }
-    return t;
-}
-
-// The same of 256 keys, four per lane.
-__device__ __forceinline__ uint32_t nth_key(u32x4 key, int n)
-{
-    uint32_t t = 0;
-    for (int b = 31; b >= 16; --b) {
-        const uint32_t c = t | (1u << b);
-        if (__popcll(__ballot(key.x >= c)) + __popcll(__ballot(key.y >= c)) +
-                __popcll(__ballot(key.z >= c)) + __popcll(__ballot(key.w >= c)) >= n)
-            t = c;
-    }
-    return t;
 }
 
 // f(rank, key) for the first n of `count` different keys in LDS (0: none), by
