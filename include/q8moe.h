@@ -796,9 +796,9 @@ int residual_norm_rows(const residual_norm_desc *desc, int64_t m, int64_t n, voi
  * logprob -infinity, kept 0; a row with a NaN or +infinity: id -1, logprob NaN,
  * kept 0.
  * Weights and sums are those of 64-bit arithmetic: weights within 1.5e-14, summed
- * as whole multiples of 2^-52 of the largest weight, or of 2^-61 to 2^-60 of the
- * row's sum where that is more, so that results do not depend on the order of a
- * sum.
+ * as whole multiples of 2^-52 of the largest weight, or of 2^-60 of the row's sum
+ * where that is more (with top-k, or min-p alone: of 2^-60 of n_vocab), so that
+ * results do not depend on the order of a sum: the same bits at every call.
  *   logits   [m][row_stride], aligned to the element, row_stride >= n_vocab when
  *            m > 1 (rows need no padding)
  * m >= 0, n_vocab > 0 (Q8_E_SHAPE); n_vocab <= 2^24, m <= 2^23, strides <= 2^32

@@ -12,13 +12,18 @@
 // exact, whatever their order, and a border of top-p or of the random number
 // falls between tokens as it does in 64 bits.
 //
-// The logits are read once.  A workgroup holds a row, or a part of one, in its
-// registers, sums its weights where a filter needs the sum, and lists the logits
-// that reach a bound: that many of its lanes' maxima do.  The list is a head of
-// the row's order (down to the largest bound of its parts), and where the
-// answers lie in it, as they do for most rows, it alone is looked at further.
-// Else (a target beyond the list, many equal logits) the row is read again, once
-// per 11 bits of each answer.
+// The logits are read once.  A workgroup takes a row, or a part of one, sums its
+// weights where a filter needs the sum, and lists the logits that reach a bound:
+// that many of its lanes' maxima do.  The list is a head of the row's order (down
+// to the largest bound of its parts), and where the answers lie in it, as they do
+// for most rows, it alone is looked at further.  The other rows (a head that goes
+// beyond the list, many equal logits) are read again: for a histogram of all
+// their weights, by as many workgroups as there are parts where rows are long,
+// and for the logits of each bin that holds an answer.
+//
+// A sum in 64 bits costs 20 vector instructions a logit, one in 32 bits 7.  For
+// top-p the latter is enough where the answer is the same over the range of its
+// error; the few rows where it is not are read again.
 #include "i8_device.h"
 #include "order_device.h"
 #include "q8_ops.h"
@@ -31,14 +36,19 @@ typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 typedef unsigned long long u64;
 
 constexpr float kReach = 64.0f;   // a histogram by value covers weights down to 2^-64
-constexpr int kPlaces = 128;      // listed logits per wave of a part
+constexpr int kPlaces = 512;      // listed logits of a part
+constexpr int kRank = 128;        // how many maxima reach a list's bound, of 256: at most
 
-// 2^t for t <= 0, off by 1.5e-14 at most: 2^r on [-1/2, 1/2] as a polynomial of
-// degree 9 that is 1 at 0 (the coefficients by the exchange algorithm).
+// 2^t for t <= 0 (2^-1000 below -1000), off by 1.5e-14 at most: 2^r on [-1/2, 1/2]
+// as a polynomial of degree 9 that is 1 at 0 (the coefficients by the exchange
+// algorithm).  The nearest whole number comes from a sum with 1.5 * 2^52, whose
+// low bits hold it: the conversions, rounding and scaling instructions of fp64
+// issue at a quarter of the rate of its sums and products.
 __device__ __forceinline__ double exp2_64(double t)
 {
-    t = fmax(t, -1100.0);
-    const double n = rint(t), r = t - n;
+    constexpr double kWhole = 0x1.8p52;
+    t = fmax(t, -1000.0);
+    const double y = t + kWhole, r = t - (y - kWhole);
     double p = 0x1.b3de7e08233fap-24;
     p = fma(p, r, 0x1.63e6984270859p-20);
     p = fma(p, r, 0x1.ffce2f62db0e4p-17);
@@ -49,7 +59,8 @@ __device__ __forceinline__ double exp2_64(double t)
     p = fma(p, r, 0x1.ebfbdff81bdf6p-3);
     p = fma(p, r, 0x1.62e42fefa37d2p-1);
     p = fma(p, r, 1.0);
-    return __builtin_amdgcn_ldexp(p, (int)n);
+    const u32x2 n = __builtin_bit_cast(u32x2, y), v = __builtin_bit_cast(u32x2, p);
+    return __builtin_bit_cast(double, (u32x2){v.x, v.y + (n.x << 20)});
 }
 
 constexpr uint32_t kLeastKey = 0x00800000u;       // value_key of the lowest finite value
@@ -79,10 +90,22 @@ struct Settings {
         top_p = p < 1.0f ? fmax((double)p, 0.0) : 1.0;
         least = m > 0.0f ? fmin(log2((double)m), 0.0) : -INFINITY;
     }
-    // whether the mass of the whole row is asked for (where k does not reach
-    // all finite logits, that of its head is)
-    __device__ __forceinline__ bool needs_sum() const { return !greedy && top_k == 0; }
+    // The sum of a row's weights: not needed where a head of the order is cut
+    // without it; in 32 bits for a share of it; in 64 bits as the mass of a row
+    // that nothing cuts (and where a scale does not fit 32 bits).
+    enum Sum { kNone, kRough, kFull };
+    __device__ __forceinline__ Sum sum() const
+    {
+        if (greedy || top_k > 0 || (top_p >= 1.0 && least > -INFINITY)) return kNone;
+        return top_p < 1.0 && scale > 1e-30 && scale < 1e30 ? kRough : kFull;
+    }
 };
+
+// How far a rough sum may be off, relative: with |t| the distance to the largest
+// logit in powers of two, a term carries 3 2^-24 ln 2 |t| (difference, scale,
+// product) and 2^-23 (the exponential), and the weights' mean of |t| over a part
+// of n logits is below log2(n) <= 14; sums of 8 add 7 2^-24: 2.3e-6 in all.
+constexpr double kRoughError = 0x1p-18;
 
 // What the weights of a row are formed with.
 struct Weights {
@@ -98,10 +121,11 @@ struct Weights {
         unit = __builtin_amdgcn_ldexp(1.0, 52 - bits);
     }
     __device__ __forceinline__ double t(float x) const { return ((double)x - (double)top) * scale; }
-    __device__ __forceinline__ u64 units(float x) const
+    __device__ __forceinline__ u64 units_at(double t) const
     {
-        return __builtin_bit_cast(u64, exp2_64(t(x)) + unit) - __builtin_bit_cast(u64, unit);
+        return __builtin_bit_cast(u64, exp2_64(t) + unit) - __builtin_bit_cast(u64, unit);
     }
+    __device__ __forceinline__ u64 units(float x) const { return units_at(t(x)); }
 };
 
 struct Head {                     // tokens at the head of the order
@@ -114,22 +138,24 @@ struct Head {                     // tokens at the head of the order
 
 template <int NT>
 struct __align__(16) Shared {
-    static constexpr int kBins = 2 * NT;               // of a histogram of the row
-    static constexpr int kBinBits = NT == 1024 ? 11 : 9;
-    static constexpr int kList = 4 * NT;               // logits of a list
-    static constexpr int kMembers = NT;                // of one bin of a list
+    static constexpr int kBins = NT == 1024 ? 2048 : 1024;    // of a histogram of the row
+    static constexpr int kBinBits = NT == 1024 ? 11 : 10;
+    static constexpr int kList = NT == 1024 ? 4096 : 2048;    // logits of a list
+    static constexpr int kMembers = NT == 1024 ? 512 : 256;   // of one bin of a list
     static_assert(NT == 1024 || NT == 256, "bins by powers of two");
     union {
         uint32_t keys[256];
-        struct {
+        struct {                  // a list, in bins by value
             u64 list[kList], mass[NT], member_key[kMembers], member_mass[kMembers];
             uint32_t count[NT];
         };
-        struct {                  // of the whole row; of one of its bins and less
-            u64 first_mass[kBins], next_mass[kBins];
-            uint32_t first_count[kBins], next_count[kBins];
+        struct {                  // a histogram of part of the row
+            u64 next_mass[kBins];
+            uint32_t next_count[kBins];
         };
     };
+    u64 first_mass[kBins];        // of the whole row
+    uint32_t first_count[kBins];
     u64 part[NT / 64];
     Head wave[NT / 64];
     Head before;                  // the answers of find() and list_locate()
@@ -157,14 +183,22 @@ template <int T, int NT, class F>
 __device__ __forceinline__ void each(const SampleArgs &a, int64_t row, F f)
 {
     typedef typename Elem<T>::type E;
-    constexpr int V = kVec<T>;
+    constexpr int V = kVec<T>, kAhead = 4;
     const E *x = (const E *)a.logits + row * a.row_stride;
     const int len = (int)a.n_vocab, vecs = len / V;
-    for (int v = threadIdx.x; v < vecs; v += NT) {
-        float y[V];
-        unpack16<T>(*(const u32x4_any *)(x + v * V), y);
+    for (int v = threadIdx.x; v < vecs; v += kAhead * NT) {
+        u32x4 raw[kAhead];
 #pragma unroll
-        for (int j = 0; j < V; ++j) f(y[j], v * V + j);
+        for (int u = 0; u < kAhead; ++u) raw[u] = *(const u32x4_any *)(x + min(v + u * NT, vecs - 1) * V);
+#pragma unroll 1
+        for (int u = 0; u < kAhead; ++u) {
+            if (v + u * NT >= vecs) break;
+            float y[V];
+            unpack16<T>(raw[0], y);
+            raw[0] = raw[1]; raw[1] = raw[2]; raw[2] = raw[3];
+#pragma unroll
+            for (int j = 0; j < V; ++j) f(y[j], (v + u * NT) * V + j);
+        }
     }
     const int i = vecs * V + threadIdx.x;
     if (i < len) f((float)x[i], i);
@@ -225,86 +259,9 @@ __device__ void find(Shared<NT> &s, const uint32_t *count, const u64 *mass, Head
     __syncthreads();
 }
 
-// Where the order reaches a target: the value there, how many of its equals are
-// needed, and the head up to and with them.
-struct Place {
-    uint32_t key, equals;
-    Head head;
-};
-
-template <int T, int NT>
-__device__ Place locate(const SampleArgs &a, int64_t row, const Weights &w, float bin_scale, Shared<NT> &s,
-                        bool by_mass, u64 target)
+__device__ __forceinline__ u64 mass_target(double share, double mass)
 {
-    constexpr int kBins = Shared<NT>::kBins;
-    find<NT>(s, s.first_count, s.first_mass, {0, 0}, by_mass, target);
-    const int first = s.bin;
-    Head before = s.before;
-    // keys that the bin may hold, a bin's width to spare on either side
-    auto bound = [&](double d) { return value_key((float)((double)w.top - d / (double)bin_scale)); };
-    uint32_t hi = first <= 0 ? value_key(w.top) : min(value_key(w.top), bound(first - 1.0));
-    uint32_t lo = first == kBins - 1 || bin_scale == 0.0f ? kLeastKey : max(kLeastKey, bound(first + 2.0));
-    while (lo != hi) {            // kBinBits of the key a turn
-        const int shift = max(0, 32 - __clz(hi - lo) - Shared<NT>::kBinBits);
-        __syncthreads();
-        for (int i = threadIdx.x; i < kBins; i += NT) {
-            s.next_count[i] = 0;
-            s.next_mass[i] = 0;
-        }
-        __syncthreads();
-        each<T, NT>(a, row, [&](float x, int) {
-            const uint32_t k = value_key(x);
-            if (k < lo || k > hi) return;
-            if ((int)fminf((w.top - x) * bin_scale, (float)(kBins - 1)) != first) return;
-            atomicAdd(&s.next_count[(hi - k) >> shift], 1u);
-            atomicAdd(&s.next_mass[(hi - k) >> shift], w.units(x));
-        });
-        find<NT>(s, s.next_count, s.next_mass, before, by_mass, target);
-        before = s.before;
-        const uint32_t top = hi - ((uint32_t)s.bin << shift);
-        lo = max(lo, top - ((1u << shift) - 1));
-        hi = top;
-    }
-    const u64 one = w.units(value_of(hi));
-    Place p;
-    p.key = hi;
-    p.equals = by_mass ? (uint32_t)((target - before.mass + one - 1) / one) : (uint32_t)(target - before.count);
-    p.head = {before.count + p.equals, before.mass + p.equals * one};
-    return p;
-}
-
-// Index of the nth (from 1) logit of the row that has this key.
-template <int T, int NT>
-__device__ int nth_equal(const SampleArgs &a, int64_t row, uint32_t key, uint32_t nth, Shared<NT> &s)
-{
-    typedef typename Elem<T>::type E;
-    const E *x = (const E *)a.logits + row * a.row_stride;
-    const int len = (int)a.n_vocab, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t before = 0;
-    if (threadIdx.x == 0) s.index = 0;
-    for (int i0 = 0; i0 < len; i0 += NT) {
-        const int i = i0 + threadIdx.x;
-        const bool eq = i < len && value_key((float)x[i]) == key;
-        const u64 in = __ballot(eq);
-        __syncthreads();
-        if (lane == 0) s.part[wave] = __popcll(in);
-        __syncthreads();
-        uint32_t rank = before + __popcll(in & ((1ull << lane) - 1)), all = 0;
-        for (int w = 0; w < NT / 64; ++w) {
-            if (w < wave) rank += (uint32_t)s.part[w];
-            all += (uint32_t)s.part[w];
-        }
-        if (eq && rank + 1 == nth) s.index = i;
-        before += all;
-        if (before >= nth) break;
-    }
-    __syncthreads();
-    return s.index;
-}
-
-__device__ __forceinline__ u64 mass_target(double share, u64 mass)
-{
-    const u64 t = (u64)ceil(share * (double)mass);
+    const u64 t = (u64)ceil(share * mass);
     return t > 0 ? t : 1;
 }
 
@@ -312,278 +269,452 @@ __device__ __forceinline__ u64 mass_target(double share, u64 mass)
 __device__ __forceinline__ u64 draw_target(float u, u64 mass)
 {
     if (u >= 1.0f) return mass;
-    const u64 t = (u64)((u > 0.0f ? (double)u : 0.0) * (double)mass) + 1;     // (NaN as 0)
-    return t < mass ? t : mass;
+    return min((u64)((u > 0.0f ? (double)u : 0.0) * (double)mass) + 1, mass);   // (NaN as 0)
 }
 
-__device__ __forceinline__ void answer(const SampleArgs &a, int64_t row, const Weights &w, uint32_t key,
-                                       int index, const Head &head)
+__device__ __forceinline__ void answer(const SampleArgs &a, int64_t row, const Weights &w, u64 key,
+                                       const Head &head)
+{
+    a.ids[row] = key_index(key);
+    a.kept[row] = (int32_t)head.count;
+    const double lp = (w.t(key_value(key)) - (log2((double)head.mass) - w.bits)) * 0.693147180559945309417;
+    a.logprob[row] = (float)fmin(lp, 0.0);
+}
+
+__device__ __forceinline__ void greedy_answer(const SampleArgs &a, int64_t row, int index)
 {
     a.ids[row] = index;
-    a.kept[row] = (int32_t)head.count;
-    const double lp = (w.t(value_of(key)) - (log2((double)head.mass) - w.bits)) * 0.693147180559945309417;
-    a.logprob[row] = (float)fmin(lp, 0.0);
+    a.kept[row] = 1;
+    a.logprob[row] = 0.0f;
 }
 
 // What every answer of a row starts from.
 struct Row {
     float top;                    // the largest logit
     uint32_t finite, bad;         // how many are finite; whether one is NaN or +infinity
-    double sum;                   // of the weights, where the settings need it
+    double sum;                   // of the weights, as the settings have it
     uint32_t bound;               // the list has all logits with keys from here on
     int listed;
 };
 
-// Rows that no list answers: the row is read again for every step.
-template <int T, int NT>
-__device__ void whole_row(const SampleArgs &a, int64_t row, const Settings &set, const Row &r, Shared<NT> &s)
-{
-    if (set.greedy) {
-        const int i = nth_equal<T, NT>(a, row, value_key(r.top), 1, s);
-        if (threadIdx.x == 0) {
-            a.ids[row] = i;
-            a.kept[row] = 1;
-            a.logprob[row] = 0.0f;
-        }
-        return;
-    }
-    constexpr int kBins = Shared<NT>::kBins;
-    double sum = r.sum;
-    if (!set.needs_sum()) {
-        const Weights w(r.top, set.scale, 1.0);
-        sum = 0.0;
-        each<T, NT>(a, row, [&](float x, int) { sum += exp2_64(w.t(x)); });
-        sum = block_sum<NT>(sum, s.part);
-    }
-    const Weights w(r.top, set.scale, sum);
-    const float bin_scale = (float)fmin(w.scale * ((kBins - 1) / kReach), 1e30);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += NT) {
-        s.first_count[i] = 0;
-        s.first_mass[i] = 0;
-    }
-    __syncthreads();
-    Head least = {0, 0};                       // the tokens that min-p keeps
-    each<T, NT>(a, row, [&](float x, int) {
-        if (!(x > -INFINITY)) return;
-        const int b = (int)fminf((w.top - x) * bin_scale, (float)(kBins - 1));
-        const u64 m = w.units(x);
-        atomicAdd(&s.first_count[b], 1u);
-        atomicAdd(&s.first_mass[b], m);
-        if (w.t(x) >= set.least) {
-            ++least.count;
-            least.mass += m;
-        }
-    });
-    least.count = (uint32_t)block_sum<NT>((u64)least.count, s.part);
-    least.mass = block_sum<NT>(least.mass, s.part);
-    Head head = {r.finite, 0};
-    for (int i = threadIdx.x; i < kBins; i += NT) head.mass += s.first_mass[i];
-    head.mass = block_sum<NT>(head.mass, s.part);
-    if (set.top_k > 0 && set.top_k < r.finite)
-        head = locate<T, NT>(a, row, w, bin_scale, s, false, set.top_k).head;
-    if (set.top_p < 1.0)
-        head = locate<T, NT>(a, row, w, bin_scale, s, true, mass_target(set.top_p, head.mass)).head;
-    if (least.count < head.count) head = least;
-    const Place at = locate<T, NT>(a, row, w, bin_scale, s, true, draw_target(set.u, head.mass));
-    const int i = nth_equal<T, NT>(a, row, at.key, at.equals, s);
-    if (threadIdx.x == 0) answer(a, row, w, at.key, i, head);
-}
-
 // ---------------------------------------------------------------------------
-// The list of a row, in s.list.
+// The logits of a list, some per thread, in bins by value: a bin per thread.
+template <int NT>
+struct Listed {
+    static constexpr int N = Shared<NT>::kList / NT;
+    u64 key[N], mass[N];
+    int bin[N];
+    Head h, own;                  // the head before this thread's bin; the bin
+    u64 end;                      // the mass of the head with the whole list
 
-// Where the list reaches a target: its key and the head up to and with it in
-// s.key and s.before.  h: the head before the thread's bin; own: the bin's.
-// False: too many logits in that bin.
-template <int NT, int N>
-__device__ bool list_locate(Shared<NT> &s, const Head &h, const Head &own, const u64 (&key)[N],
-                            const u64 (&mass)[N], const int (&bin)[N], bool by_mass, u64 target)
-{
-    __syncthreads();
-    if (threadIdx.x == 0) s.members = 0;
-    const Head next = {h.count + own.count, h.mass + own.mass};
-    if (!reaches(h, by_mass, target) && reaches(next, by_mass, target)) {
-        s.bin = threadIdx.x;
-        s.before = h;
+    __device__ __forceinline__ void take(Shared<NT> &s, int n)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = threadIdx.x + i * NT;
+            key[i] = at < n ? s.list[at] : 0;
+        }
     }
-    __syncthreads();
-    const int b = s.bin;
-    const Head before = s.before;
+    // high, low: no listed value is outside; before: the head before the list
+    __device__ void sort(Shared<NT> &s, const Weights &w, float high, float low, Head before)
+    {
+        const float reach = fminf(high - low, (float)(kReach / w.scale));
+        const float bin_scale = fminf((float)(NT - 1) / reach, 1e30f);
+        __syncthreads();
+        s.count[threadIdx.x] = 0;
+        s.mass[threadIdx.x] = 0;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (bin[i] == b) {
-            const int at = atomicAdd(&s.members, 1);
-            if (at < Shared<NT>::kMembers) {
-                s.member_key[at] = key[i];
-                s.member_mass[at] = mass[i];
+        for (int i = 0; i < N; ++i) {
+            bin[i] = -1;
+            mass[i] = 0;
+            if (key[i]) {
+                const float x = key_value(key[i]);
+                mass[i] = w.units(x);
+                bin[i] = (int)fminf((high - x) * bin_scale, (float)(NT - 1));
+                atomicAdd(&s.count[bin[i]], 1u);
+                atomicAdd(&s.mass[bin[i]], mass[i]);
             }
         }
-    __syncthreads();
-    const int n = s.members;
-    if (n > Shared<NT>::kMembers) return false;
+        __syncthreads();
+        own = {s.count[threadIdx.x], s.mass[threadIdx.x]};
+        h = scan<NT>(s, before, own);
+        if (threadIdx.x == NT - 1) s.before = {0, h.mass + own.mass};
+        __syncthreads();
+        end = s.before.mass;
+    }
+    // Where the order reaches a target: its key and the head up to and with it in
+    // s.key and s.before.  False: not in the list, or too many logits in a bin.
+    __device__ bool locate(Shared<NT> &s, bool by_mass, u64 target) const
+    {
+        if (by_mass && target > end) return false;
+        __syncthreads();
+        if (threadIdx.x == 0) s.members = 0;
+        const Head next = {h.count + own.count, h.mass + own.mass};
+        if (!reaches(h, by_mass, target) && reaches(next, by_mass, target)) {
+            s.bin = threadIdx.x;
+            s.before = h;
+        }
+        __syncthreads();
+        const int b = s.bin;
+        const Head before = s.before;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (bin[i] == b) {
-            Head ahead = before;
-            for (int j = 0; j < n; ++j)
-                if (s.member_key[j] > key[i]) {
-                    ++ahead.count;
-                    ahead.mass += s.member_mass[j];
+        for (int i = 0; i < N; ++i)
+            if (bin[i] == b) {
+                const int at = atomicAdd(&s.members, 1);
+                if (at < Shared<NT>::kMembers) {
+                    s.member_key[at] = key[i];
+                    s.member_mass[at] = mass[i];
                 }
-            const Head with = {ahead.count + 1, ahead.mass + mass[i]};
-            if (!reaches(ahead, by_mass, target) && reaches(with, by_mass, target)) {
-                s.key = key[i];
-                s.before = with;
             }
-        }
-    __syncthreads();
-    return true;
-}
+        __syncthreads();
+        const int n = s.members;
+        if (n > Shared<NT>::kMembers) return false;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (bin[i] == b) {
+                Head ahead = before;
+                for (int j = 0; j < n; ++j)
+                    if (s.member_key[j] > key[i]) {
+                        ++ahead.count;
+                        ahead.mass += s.member_mass[j];
+                    }
+                const Head with = {ahead.count + 1, ahead.mass + mass[i]};
+                if (!reaches(ahead, by_mass, target) && reaches(with, by_mass, target)) {
+                    s.key = key[i];
+                    s.before = with;
+                }
+            }
+        __syncthreads();
+        return true;
+    }
+    // The listed tokens that min-p keeps.
+    __device__ Head least(Shared<NT> &s, const Weights &w, double least) const
+    {
+        Head l = {0, 0};
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (key[i] && w.t(key_value(key[i])) >= least) {
+                ++l.count;
+                l.mass += mass[i];
+            }
+        l.count = (uint32_t)block_sum<NT>((u64)l.count, s.part);
+        l.mass = block_sum<NT>(l.mass, s.part);
+        return l;
+    }
+};
 
 // The row's answers from its list; false where they do not lie in it.
 template <int NT>
-__device__ bool from_list(const SampleArgs &a, int64_t row, const Settings &set, const Row &r, Shared<NT> &s)
+__device__ bool from_list(const SampleArgs &a, int64_t row, const Settings &set, const Row &r, Shared<NT> &s,
+                          Listed<NT> &l)
 {
-    constexpr int kList = Shared<NT>::kList, N = kList / NT;
     const int tid = threadIdx.x, n = r.listed;
-    if (n == 0 || n > kList) return false;
-    const bool all = (uint32_t)n == r.finite;
-    if (set.top_k > 0 && set.top_k < r.finite && set.top_k > (uint32_t)n) return false;
+    const bool all = (uint32_t)n == r.finite, cut = set.top_k > 0 && set.top_k < r.finite;
+    if (cut && set.top_k > (uint32_t)n) return false;
     if (set.greedy) {                          // the largest key
         u64 best = 0;
-        for (int i = tid; i < n; i += NT) best = max(best, s.list[i]);
+#pragma unroll
+        for (int i = 0; i < Listed<NT>::N; ++i) best = max(best, l.key[i]);
 #pragma unroll
         for (int d = 32; d; d >>= 1) best = max(best, (u64)__shfl_xor(best, d));
         if ((tid & 63) == 0) s.part[tid >> 6] = best;
         __syncthreads();
         if (tid == 0) {
             for (int w = 1; w < NT / 64; ++w) best = max(best, s.part[w]);
-            a.ids[row] = key_index(best);
-            a.kept[row] = 1;
-            a.logprob[row] = 0.0f;
+            greedy_answer(a, row, key_index(best));
         }
         return true;
     }
+    const Settings::Sum sum = set.sum();
     const float low = value_of(r.bound);
-    const Weights w(r.top, set.scale, set.needs_sum() ? r.sum : (double)n);
-    // bins by value, a bin per thread, down to the bound or to weights of 2^-64
-    const float reach = fminf(r.top - low, (float)(kReach / set.scale));
-    const float bin_scale = fminf((float)(NT - 1) / reach, 1e30f);
-    s.count[tid] = 0;
-    s.mass[tid] = 0;
-    __syncthreads();
-    u64 key[N], mass[N];
-    int bin[N];
-    Head least = {0, 0};
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        bin[i] = -1;
-        key[i] = mass[i] = 0;
-        if (tid + i * NT < n) {
-            key[i] = s.list[tid + i * NT];
-            const float x = key_value(key[i]);
-            mass[i] = w.units(x);
-            bin[i] = (int)fminf((w.top - x) * bin_scale, (float)(NT - 1));
-            atomicAdd(&s.count[bin[i]], 1u);
-            atomicAdd(&s.mass[bin[i]], mass[i]);
-            if (w.t(x) >= set.least) {
-                ++least.count;
-                least.mass += mass[i];
-            }
+    const Weights w(r.top, set.scale, sum != Settings::kNone ? r.sum : (double)n);
+    l.sort(s, w, r.top, low, {0, 0});
+    // the head so far, the mass that shares are of and how far it may be off
+    Head head = {r.finite, l.end};
+    double mass = (double)l.end, off = 0.0;
+    bool whole = !all;                         // the head goes beyond the list
+    if (!all && sum != Settings::kNone) {
+        mass = r.sum * __builtin_amdgcn_ldexp(1.0, w.bits);
+        head.mass = (u64)mass;
+        off = sum == Settings::kRough ? kRoughError : 0.0;
+    }
+#pragma unroll 1
+    for (int step = 0; step < 3; ++step) {     // top-k, top-p, the draw
+        u64 target = set.top_k;
+        if (step == 0 && !cut) continue;
+        if (step == 1) {
+            if (set.top_p >= 1.0) continue;
+            if (whole && sum == Settings::kNone) return false;      // (top-k of all there are)
+            target = mass_target(set.top_p, mass * (1.0 - off));
         }
-    }
-    __syncthreads();
-    const Head own = {s.count[tid], s.mass[tid]};
-    const Head h = scan<NT>(s, {0, 0}, own);
-    if (tid == NT - 1) s.before = {0, h.mass + own.mass};
-    __syncthreads();
-    const u64 listed_mass = s.before.mass;
-    Head head = {r.finite, listed_mass};
-    if (!all && set.needs_sum()) head.mass = (u64)(r.sum * __builtin_amdgcn_ldexp(1.0, w.bits));
-    if (set.top_k > 0 && set.top_k < r.finite) {
-        if (!list_locate<NT, N>(s, h, own, key, mass, bin, false, set.top_k)) return false;
+        if (step == 2) {
+            // the tokens that min-p keeps are all listed, or all that is listed is among them
+            if (set.least > -INFINITY && (all || w.t(low) < set.least)) {
+                const Head least = l.least(s, w, set.least);
+                if (least.count < head.count) {
+                    head = least;
+                    whole = false;
+                }
+            }
+            if (whole && sum != Settings::kFull) return false;
+            target = draw_target(set.u, head.mass);
+        }
+        if (!l.locate(s, step > 0, target)) return false;
+        if (step == 2) break;
         head = s.before;
-    } else if (!all && !set.needs_sum())
-        return false;                          // top-k of more than there are
-    if (set.top_p < 1.0) {
-        const u64 target = mass_target(set.top_p, head.mass);
-        if (target > listed_mass || !list_locate<NT, N>(s, h, own, key, mass, bin, true, target)) return false;
-        head = s.before;
+        if (step == 1 && head.mass < mass_target(set.top_p, mass * (1.0 + off))) return false;
+        mass = (double)head.mass;
+        off = 0.0;
+        whole = false;
     }
-    if (set.least > -INFINITY) {
-        // the tokens that min-p keeps are all listed, or all that is listed is among them
-        if (all || w.t(low) < set.least) {
-            least.count = (uint32_t)block_sum<NT>((u64)least.count, s.part);
-            least.mass = block_sum<NT>(least.mass, s.part);
-            if (least.count < head.count) head = least;
-        } else if (head.count > (uint32_t)n)
-            return false;
-    }
-    const u64 target = draw_target(set.u, head.mass);
-    if (target > listed_mass || !list_locate<NT, N>(s, h, own, key, mass, bin, true, target)) return false;
-    if (tid == 0) answer(a, row, w, (uint32_t)(s.key >> 32), key_index(s.key), head);
+    if (tid == 0) answer(a, row, w, s.key, head);
     return true;
 }
 
+// ---------------------------------------------------------------------------
+// Rows that the list does not answer.
+
+// Index of the nth (from 1) logit of the row that has this key: the waves count
+// a stretch each, and the one that has it looks for it.
 template <int T, int NT>
-__device__ void row_answers(const SampleArgs &a, int64_t row, const Settings &set, const Row &r, Shared<NT> &s)
+__device__ int nth_equal(const SampleArgs &a, int64_t row, uint32_t key, uint32_t nth, Shared<NT> &s)
 {
-    if (r.bad || !r.finite) {
-        if (threadIdx.x == 0) {
-            a.ids[row] = -1;
-            a.kept[row] = 0;
-            a.logprob[row] = r.bad ? __builtin_nanf("") : -INFINITY;
+    typedef typename Elem<T>::type E;
+    const E *x = (const E *)a.logits + row * a.row_stride;
+    const int len = (int)a.n_vocab, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = ((len + NT - 1) / NT) * 64, begin = min(wave * per, len), end = min(begin + per, len);
+    uint32_t count = 0;
+#pragma unroll 8
+    for (int i = begin + lane; i < end; i += 64) count += value_key((float)x[i]) == key;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) count += __shfl_xor(count, d);
+    __syncthreads();
+    if (threadIdx.x == 0) s.index = 0;
+    if (lane == 0) s.part[wave] = count;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < wave; ++w) before += (uint32_t)s.part[w];
+    if (before < nth && nth <= before + count)
+        for (int i0 = begin; i0 < end; i0 += 64) {
+            const bool eq = i0 + lane < end && value_key((float)x[i0 + lane]) == key;
+            const u64 in = __ballot(eq);
+            if (eq && before + __popcll(in & ((1ull << lane) - 1)) + 1 == nth) s.index = i0 + lane;
+            before += __popcll(in);
+            if (before >= nth) break;
         }
+    __syncthreads();
+    return s.index;
+}
+
+// Where the order reaches a target, from the row: the key with its index in s.key
+// (`index`), and the head up to and with it, returned.  known: the row's list,
+// which has all keys from `known_from` on.
+template <int T, int NT>
+__device__ __forceinline__ Head locate(const SampleArgs &a, int64_t row, const Weights &w, float bin_scale,
+                                       Shared<NT> &s, const Listed<NT> &known, uint32_t known_from,
+                                       bool by_mass, u64 target, bool index)
+{
+    constexpr int kBins = Shared<NT>::kBins;
+    find<NT>(s, s.first_count, s.first_mass, {0, 0}, by_mass, target);
+    const int first = s.bin;
+    uint32_t count = s.first_count[first];
+    Head before = s.before;
+    // keys that the bin may hold, a bin's width to spare on either side
+    auto bound = [&](double d) { return value_key((float)((double)w.top - d / (double)bin_scale)); };
+    uint32_t hi = first <= 0 ? value_key(w.top) : min(value_key(w.top), bound(first - 1.0));
+    uint32_t lo = first == kBins - 1 || bin_scale == 0.0f ? kLeastKey : max(kLeastKey, bound(first + 2.0));
+    auto inside = [&](float x, uint32_t k) {
+        return k >= lo && k <= hi && (int)fminf((w.top - x) * bin_scale, (float)(kBins - 1)) == first;
+    };
+    while (lo != hi) {
+        __syncthreads();
+        if (count <= Shared<NT>::kList) {      // its logits as a list
+            if (threadIdx.x == 0) s.listed = 0;
+            __syncthreads();
+            auto take = [&](float x, u64 key) {
+                if (!inside(x, (uint32_t)(key >> 32))) return;
+                const int at = atomicAdd(&s.listed, 1);
+                if (at < Shared<NT>::kList) s.list[at] = key;
+            };
+            if (lo >= known_from) {
+                for (int i = 0; i < Listed<NT>::N; ++i)
+                    if (known.key[i]) take(key_value(known.key[i]), known.key[i]);
+            } else
+                each<T, NT>(a, row, [&](float x, int i) { take(x, order_key(x, (uint32_t)i)); });
+            __syncthreads();
+            Listed<NT> l;
+            l.take(s, (int)count);
+            l.sort(s, w, value_of(hi), value_of(lo), before);
+            if (l.locate(s, by_mass, target)) return s.before;
+            __syncthreads();
+            count = Shared<NT>::kList + 1;
+        }
+        // else in bins by key, kBinBits of it a turn
+        const int shift = max(0, 32 - __clz(hi - lo) - Shared<NT>::kBinBits);
+        for (int i = threadIdx.x; i < kBins; i += NT) {
+            s.next_count[i] = 0;
+            s.next_mass[i] = 0;
+        }
+        __syncthreads();
+        each<T, NT>(a, row, [&](float x, int) {
+            const uint32_t k = value_key(x);
+            if (!inside(x, k)) return;
+            atomicAdd(&s.next_count[(hi - k) >> shift], 1u);
+            atomicAdd(&s.next_mass[(hi - k) >> shift], w.units(x));
+        });
+        find<NT>(s, s.next_count, s.next_mass, before, by_mass, target);
+        before = s.before;
+        count = s.next_count[s.bin];
+        const uint32_t top = hi - ((uint32_t)s.bin << shift);
+        lo = max(lo, top - ((1u << shift) - 1));
+        hi = top;
+    }
+    const u64 one = w.units(value_of(hi));
+    const uint32_t equals = by_mass ? (uint32_t)((target - before.mass + one - 1) / one)
+                                    : (uint32_t)(target - before.count);
+    if (index) {
+        const int i = nth_equal<T, NT>(a, row, hi, equals, s);
+        if (threadIdx.x == 0) s.key = order_key(value_of(hi), (uint32_t)i);
+    }
+    return {before.count + equals, before.mass + equals * one};
+}
+
+// The histogram of a row by value.
+__device__ __forceinline__ float row_bin_scale(const Weights &w, int bins)
+{
+    return (float)fmin(w.scale * ((bins - 1) / kReach), 1e30);
+}
+
+template <int BINS>
+struct RowBins {
+    const Weights &w;
+    float bin_scale;
+    double least;
+    Head kept;                    // the tokens that min-p keeps, of this thread
+    __device__ __forceinline__ RowBins(const Weights &w, double least)
+        : w(w), bin_scale(row_bin_scale(w, BINS)), least(least), kept({0, 0})
+    {
+    }
+    __device__ __forceinline__ void add(float x, uint32_t *count, u64 *mass)
+    {
+        if (!(x > -INFINITY)) return;
+        const int b = (int)fminf((w.top - x) * bin_scale, (float)(BINS - 1));
+        const double t = w.t(x);
+        const u64 m = w.units_at(t);
+        atomicAdd(&count[b], 1u);
+        atomicAdd(&mass[b], m);
+        if (t >= least) {
+            ++kept.count;
+            kept.mass += m;
+        }
+    }
+};
+
+// The row's answers from its histogram (s.first_*) and the row.  least: the
+// tokens that min-p keeps; l has all the row's keys from known_from on.
+template <int T, int NT>
+__device__ __forceinline__ void from_bins(const SampleArgs &a, int64_t row, const Settings &set, uint32_t finite,
+                                          const Weights &w, Head least, Shared<NT> &s, const Listed<NT> &l,
+                                          uint32_t known_from)
+{
+    constexpr int kBins = Shared<NT>::kBins;
+    Head head = {finite, 0};
+    for (int i = threadIdx.x; i < kBins; i += NT) head.mass += s.first_mass[i];
+    head.mass = block_sum<NT>(head.mass, s.part);
+#pragma unroll 1
+    for (int step = 0; step < 3; ++step) {     // top-k, top-p, the draw
+        u64 target = set.top_k;
+        if (step == 0 && (set.top_k == 0 || set.top_k >= finite)) continue;
+        if (step == 1) {
+            if (set.top_p >= 1.0) continue;
+            target = mass_target(set.top_p, (double)head.mass);
+        }
+        if (step == 2) {
+            if (least.count < head.count) head = least;
+            target = draw_target(set.u, head.mass);
+        }
+        const Head h = locate<T, NT>(a, row, w, row_bin_scale(w, kBins), s, l, known_from, step > 0, target,
+                                     step == 2);
+        if (step < 2) head = h;
+    }
+    if (threadIdx.x == 0) answer(a, row, w, s.key, head);
+}
+
+// What the units of a row are set by: its sum as far as known, else a bound (no
+// weight beyond the list is above the bound's).
+__device__ __forceinline__ double units_sum(const Settings &set, const Row &r)
+{
+    if (set.sum() != Settings::kNone) return r.sum;
+    if (r.bound == kNoBound) return (double)r.finite;
+    const double t = ((double)value_of(r.bound) - (double)r.top) * set.scale;
+    return (double)r.listed + (double)(r.finite - (uint32_t)r.listed) * exp2_64(t);
+}
+
+// The row's answers from the row itself.
+template <int T, int NT>
+__device__ __forceinline__ void from_row(const SampleArgs &a, int64_t row, const Settings &set, const Row &r,
+                                         Shared<NT> &s, const Listed<NT> &l, uint32_t known_from)
+{
+    constexpr int kBins = Shared<NT>::kBins;
+    if (set.greedy) {
+        const int i = nth_equal<T, NT>(a, row, value_key(r.top), 1, s);
+        if (threadIdx.x == 0) greedy_answer(a, row, i);
         return;
     }
-    if (from_list<NT>(a, row, set, r, s)) return;
+    const Weights w(r.top, set.scale, units_sum(set, r));
     __syncthreads();
-    whole_row<T, NT>(a, row, set, r, s);
+    for (int i = threadIdx.x; i < kBins; i += NT) {
+        s.first_count[i] = 0;
+        s.first_mass[i] = 0;
+    }
+    __syncthreads();
+    RowBins<kBins> bins(w, set.least);
+    each<T, NT>(a, row, [&](float x, int) { bins.add(x, s.first_count, s.first_mass); });
+    Head least;
+    least.count = (uint32_t)block_sum<NT>((u64)bins.kept.count, s.part);
+    least.mass = block_sum<NT>(bins.kept.mass, s.part);
+    from_bins<T, NT>(a, row, set, r.finite, w, least, s, l, known_from);
+}
+
+// A row without a distribution: true, and its answers are written.
+__device__ __forceinline__ bool no_row(const SampleArgs &a, int64_t row, const Row &r)
+{
+    if (!r.bad && r.finite) return false;
+    if (threadIdx.x == 0) {
+        a.ids[row] = -1;
+        a.kept[row] = 0;
+        a.logprob[row] = r.bad ? __builtin_nanf("") : -INFINITY;
+    }
+    return true;
 }
 
 // ---------------------------------------------------------------------------
-// Logits in registers: `E` of them a thread, of a stretch of a row.
+// A stretch of a row, 8 vectors of 16 bytes a thread, in LDS, where each thread
+// keeps its own: loops over them stay rolled and take few registers.  What is
+// left after the last whole vector is one logit a thread.
+constexpr int kVecs = 8;
 
-template <int T, int NT, int E>
+template <int T, int NT>
 struct Held {
-    static constexpr int V = kVec<T>, N = E / V;
-    u32x4 raw[N];
-    int begin;                    // index of the stretch in its row
+    static constexpr int V = kVec<T>, kLogits = kVecs * V * NT;
+    u32x4 *lds;                   // [kVecs][NT]
+    float extra;
+    int begin, extra_at;          // indices in the row
 
-    // logits begin .. begin + len - 1; those beyond are -infinity
-    __device__ __forceinline__ void load(const SampleArgs &a, int64_t row, int first, int len)
-    {
-        typedef typename Elem<T>::type El;
-        begin = first;
-        const El *x = (const El *)a.logits + row * a.row_stride + first;
-        const uint32_t none = T == Q8_T_F32 ? 0xff800000u : T == Q8_T_F16 ? 0xfc00fc00u : 0xff80ff80u;
-#pragma unroll
-        for (int v = 0; v < N; ++v) {
-            const int i = (threadIdx.x + v * NT) * V;
-            if (i + V <= len)
-                raw[v] = *(const u32x4_any *)(x + i);
-            else {
-                raw[v] = (u32x4){none, none, none, none};
-                if (i < len) {
-                    float y[V];
-#pragma unroll
-                    for (int j = 0; j < V; ++j) y[j] = i + j < len ? (float)x[i + j] : -INFINITY;
-                    raw[v] = pack_vec<T>(y);
-                }
-            }
-        }
-    }
+    // f(value, index); beyond the stretch -infinity
     template <class F>
     __device__ __forceinline__ void each(F f) const
     {
-#pragma unroll
-        for (int v = 0; v < N; ++v) {
+#pragma unroll 1
+        for (int v = 0; v < kVecs; ++v) {
             float y[V];
-            unpack16<T>(raw[v], y);
+            unpack16<T>(lds[v * NT + threadIdx.x], y);
+            const int i = begin + (int)(threadIdx.x + v * NT) * V;
 #pragma unroll
-            for (int j = 0; j < V; ++j) f(y[j], begin + (int)(threadIdx.x + v * NT) * V + j);
+            for (int j = 0; j < V; ++j) f(y[j], i + j);
         }
+        f(extra, extra_at);
     }
 };
 
@@ -595,21 +726,47 @@ struct Stretch {
     double sum;
 };
 
-template <int T, int NT, int E>
-__device__ Stretch stretch(const Held<T, NT, E> &x, const Settings &set, int len, u64 *part)
+// logits first .. first + len - 1 of the row into x and their statistics
+template <int T, int NT>
+__device__ __forceinline__ Stretch stretch(const SampleArgs &a, int64_t row, int first, int len,
+                                           const Settings &set, Held<T, NT> &x, u64 *part)
 {
-    Stretch r = {-INFINITY, -INFINITY, 0, 0, 0.0};
-    float lowest = INFINITY;
-    bool bad = false;
-    x.each([&](float v, int) {
-        r.own_top = fmaxf(r.own_top, v);
-        lowest = fminf(lowest, v);
-        bad |= v != v;
-    });
+    typedef typename Elem<T>::type El;
+    constexpr int V = kVec<T>;
+    const uint32_t none = T == Q8_T_F32 ? 0xff800000u : T == Q8_T_F16 ? 0xfc00fc00u : 0xff80ff80u;
+    const El *p = (const El *)a.logits + row * a.row_stride + first;
+    u32x4 raw[kVecs];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        const int i = (threadIdx.x + v * NT) * V;
+        raw[v] = (u32x4){none, none, none, none};
+        if (i + V <= len) raw[v] = *(const u32x4_any *)(p + i);
+    }
+    const int left = len / V * V + threadIdx.x;
+    x.begin = first;
+    x.extra_at = first + left;
+    x.extra = left < len ? (float)p[left] : -INFINITY;
+
+    Stretch r = {-INFINITY, x.extra, 0, 0, 0.0};
+    float lowest = x.extra;
+    bool bad = x.extra != x.extra;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        float y[V];
+        x.lds[v * NT + threadIdx.x] = raw[v];
+        unpack16<T>(raw[v], y);
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            r.own_top = fmaxf(fmaxf(y[j], y[j + 1]), r.own_top);
+            lowest = fminf(fminf(y[j], y[j + 1]), lowest);
+            bad |= __builtin_isunordered(y[j], y[j + 1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
     bad |= r.own_top == INFINITY;
     uint32_t finite = 0;
     if (lowest == -INFINITY) x.each([&](float v, int) { finite += v > -INFINITY; });
-    else finite = E;
+    else finite = kVecs * V + 1;
     r.top = r.own_top;
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
@@ -619,7 +776,7 @@ __device__ Stretch stretch(const Held<T, NT, E> &x, const Settings &set, int len
     const u64 any = __ballot(bad);
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0)
-        part[wave] = (u64)__builtin_bit_cast(uint32_t, r.top) << 32 | finite << 1 | (any != 0);
+        part[wave] = (u64)__builtin_bit_cast(uint32_t, r.top) << 32 | finite << 1 | (any != 0);   // (finite < 2^13)
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < NT / 64; ++w) {
@@ -627,231 +784,464 @@ __device__ Stretch stretch(const Held<T, NT, E> &x, const Settings &set, int len
         r.finite += (uint32_t)part[w] >> 1;
         r.bad |= (uint32_t)part[w] & 1;
     }
-    if (set.needs_sum() && r.top > -INFINITY && !r.bad) {
+    const Settings::Sum kind = set.sum();
+    if (kind == Settings::kNone || r.top == -INFINITY || r.bad) return r;
+    double sum = 0.0;
+    if (kind == Settings::kRough) {
+        const float scale = (float)set.scale;
+#pragma unroll 2
+        for (int v = 0; v < kVecs; ++v) {
+            float y[V], some = 0.0f;
+            unpack16<T>(x.lds[v * NT + threadIdx.x], y);
+#pragma unroll
+            for (int j = 0; j < V; ++j) some += __builtin_amdgcn_exp2f((y[j] - r.top) * scale);
+            sum += (double)some;
+        }
+        sum += (double)__builtin_amdgcn_exp2f((x.extra - r.top) * scale);
+    } else {
         // (the difference first: v * scale - top * scale would round masks near the
         // type's lowest value apart)
         const double top = r.top;
-        double sum = 0.0;
         x.each([&](float v, int) { sum += exp2_64(((double)v - top) * set.scale); });
-        r.sum = block_sum<NT>(sum, part);
     }
+    r.sum = block_sum<NT>(sum, part);
     return r;
 }
 
-// A key that `rank` or more logits of the workgroup reach: that of the rank-th
-// of 256 groups' maxima, its low half cut.
-template <int NT>
-__device__ uint32_t list_bound(float own_top, int rank, uint32_t *keys)
+// A key that `rank` or more logits of a workgroup of 256 reach: that of the
+// rank-th of its threads' maxima, its low half cut.
+__device__ __forceinline__ uint32_t list_bound(float own_top, int rank, uint32_t *keys)
 {
-    uint32_t k = value_key(own_top);
-    if constexpr (NT == 1024) {
-        k = max(k, (uint32_t)__shfl_xor((int)k, 1));
-        k = max(k, (uint32_t)__shfl_xor((int)k, 2));
-        if ((threadIdx.x & 3) == 0) keys[threadIdx.x >> 2] = k;
-    } else
-        keys[threadIdx.x] = k;
+    keys[threadIdx.x] = value_key(own_top);
     __syncthreads();
     return max(nth_key(((const u32x4 *)keys)[threadIdx.x & 63], rank), kLeastKey);
 }
 
-// ---------------------------------------------------------------------------
-// A row per workgroup.
-template <int T, int NT, int E>
-__global__ __launch_bounds__(NT) void sample_row_kernel(const SampleArgs a)
+constexpr int kPartThreads = 256;
+
+// The logits of a stretch from `low` on as keys to list(place, key), where they
+// are `most` or fewer; returns how many they are.  A thread marks its own in a
+// mask (two instructions a logit), then takes them one by one: few have any.
+template <int T, int NT, class F>
+__device__ __forceinline__ int list_stretch(const Held<T, NT> &x, float low, int most, u64 *part, F list)
 {
-    __shared__ Shared<NT> s;
-    const int64_t row = blockIdx.x;
-    const int len = (int)a.n_vocab, lane = threadIdx.x & 63;
-    Held<T, NT, E> x;
-    x.load(a, row, 0, len);
-    const Settings set(a, row);
-    if (threadIdx.x == 0) s.listed = 0;
-    const Stretch st = stretch<T, NT, E>(x, set, len, s.part);
-    Row r;
-    r.top = st.top; r.finite = st.finite; r.bad = st.bad; r.sum = st.sum;
-    r.bound = list_bound<NT>(st.own_top, 128, s.keys);
-    __syncthreads();              // (the list lies where the keys were)
-    const float low = value_of(r.bound);
-    x.each([&](float v, int i) {
-        const u64 in = __ballot(v >= low);
-        if (!in) return;
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&s.listed, (int)__popcll(in));
-        at = wave_uniform(at) + __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32),
-                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
-        if (v >= low && at < Shared<NT>::kList) s.list[at] = order_key(v, (uint32_t)i);
-    });
+    typedef typename Elem<T>::type El;
+    constexpr int V = kVec<T>;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint64_t mask = 0;            // bit V * (kVecs - v) - 1 - j: logit j of vector v
+#pragma unroll 2
+    for (int v = 0; v < kVecs; ++v) {
+        float y[V];
+        unpack16<T>(x.lds[v * NT + threadIdx.x], y);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) m = m + m + (y[j] >= low);
+        mask = mask << V | m;
+    }
+    int at = __popcll(mask) + (x.extra >= low);
+    const int mine = at;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int c = __shfl_up(at, d);
+        if (lane >= d) at += c;
+    }
+    if (lane == 63) part[wave] = (u64)at;
     __syncthreads();
-    r.listed = s.listed;
-    row_answers<T, NT>(a, row, set, r, s);
+    at -= mine;
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        if (w < wave) at += (int)part[w];
+        all += (int)part[w];
+    }
+    __syncthreads();
+    if (all > most) return all;
+    while (mask) {
+        const int bit = __builtin_ctzll(mask), from = kVecs * V - 1 - bit, v = from / V, j = from % V;
+        mask &= mask - 1;
+        const float y = (float)((const El *)(x.lds + v * NT + threadIdx.x))[j];
+        list(at++, order_key(y, (uint32_t)(x.begin + (int)(threadIdx.x + v * NT) * V + j)));
+    }
+    if (x.extra >= low) list(at, order_key(x.extra, (uint32_t)x.extra_at));
+    return all;
 }
 
-// A part of a row per workgroup, and the join of a row's parts.
-constexpr int kPartWaves = 4, kPartThreads = 64 * kPartWaves;
+// ---------------------------------------------------------------------------
+// Short rows: one per workgroup.
+template <int T>
+__global__ __launch_bounds__(kPartThreads) void sample_row_kernel(const SampleArgs a)
+{
+    constexpr int NT = kPartThreads;
+    __shared__ Shared<NT> s;
+    __shared__ u32x4 held[kVecs * NT];
+    const int64_t row = blockIdx.x;
+    const Settings set(a, row);
+    Held<T, NT> x;
+    x.lds = held;
+    const Stretch st = stretch<T, NT>(a, row, 0, (int)a.n_vocab, set, x, s.part);
+    Row r = {st.top, st.finite, st.bad, st.sum, 0, 0};
+    if (no_row(a, row, r)) return;
+#pragma unroll 1
+    for (int rank = kRank; rank > 0; rank /= 4) {       // (a smaller one where the list is full)
+        r.bound = list_bound(st.own_top, rank, s.keys);
+        __syncthreads();          // (the list lies where the keys were)
+        r.listed = list_stretch<T, NT>(x, value_of(r.bound), Shared<NT>::kList, s.part,
+                                       [&](int at, u64 key) { s.list[at] = key; });
+        if (r.listed <= Shared<NT>::kList) break;
+        __syncthreads();
+    }
+    __syncthreads();
+    Listed<NT> l;
+    const bool listed = r.listed > 0 && r.listed <= Shared<NT>::kList;
+    l.take(s, listed ? r.listed : 0);
+    if (listed && from_list<NT>(a, row, set, r, s, l)) return;
+    __syncthreads();
+    if (!listed) r.bound = kNoBound;
+    from_row<T, NT>(a, row, set, r, s, l, r.bound);
+}
+
+// ---------------------------------------------------------------------------
+// Longer rows: a part of one per workgroup, the join of its parts, and for the
+// rows that their lists do not answer a histogram by parts and its reading.
 
 struct PartOut {
     double sum;
     float top;
     uint32_t bound, finite, bad;
-    int listed[kPartWaves];
+    int listed;
+};
+
+constexpr int kRowBins = Shared<1024>::kBins, kRowList = Shared<kPartThreads>::kList;
+
+// A row that is read again.
+struct Again {
+    u64 mass[kRowBins], list[kRowList], least_mass;
+    uint32_t count[kRowBins], least_count;
+    int row;
+    Row r;
 };
 
 struct Work {
     PartOut *parts;               // [m][parts]
-    u64 *lists;                   // [m][parts][kPartWaves][kPlaces]
-    int n_parts, rank;
+    u64 *lists;                   // [m][parts][kPlaces]
+    Again *again;                 // [m], the first *n_again of them
+    int *n_again;
+    int n_parts, part_len, rank;
 };
 
-template <int T, int E>
+template <int T>
 __global__ __launch_bounds__(kPartThreads) void sample_part_kernel(const SampleArgs a, const Work w)
 {
-    __shared__ u64 part[kPartWaves];
-    __shared__ __align__(16) uint32_t keys[256];
-    __shared__ PartOut out;
+    constexpr int NT = kPartThreads;
+    __shared__ u32x4 held[kVecs * NT];
+    __shared__ u64 part[NT / 64];
+    __shared__ __align__(16) uint32_t keys[NT];
     const int64_t row = blockIdx.y;
-    const int wave = wave_uniform((int)(threadIdx.x >> 6));
-    const int first = blockIdx.x * kPartThreads * E, len = min(kPartThreads * E, (int)a.n_vocab - first);
-    Held<T, kPartThreads, E> x;
-    x.load(a, row, first, len);
+    const int first = blockIdx.x * w.part_len, len = min(w.part_len, (int)a.n_vocab - first);
+    if (row == 0 && first == 0 && threadIdx.x == 0) *w.n_again = 0;
     const Settings set(a, row);
-    const Stretch st = stretch<T, kPartThreads, E>(x, set, len, part);
-    uint32_t bound = list_bound<kPartThreads>(st.own_top, w.rank, keys);
-    const float low = value_of(bound);
+    Held<T, NT> x;
+    x.lds = held;
+    const Stretch st = stretch<T, NT>(a, row, first, len, set, x, part);
     const int64_t at = row * w.n_parts + blockIdx.x;
-    u64 *list = w.lists + (at * kPartWaves + wave) * kPlaces;
-    int listed = 0;
-    x.each([&](float v, int i) {
-        const u64 in = __ballot(v >= low);
-        if (!in) return;
-        const int p = listed + __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32),
-                                                         __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
-        if (v >= low && p < kPlaces) list[p] = order_key(v, (uint32_t)i);
-        listed += __popcll(in);
-    });
-    if ((threadIdx.x & 63) == 0) out.listed[wave] = listed;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kPartWaves; ++i)
-            if (out.listed[i] > kPlaces) bound = kNoBound;
-        out.sum = st.sum; out.top = st.top; out.bound = bound; out.finite = st.finite; out.bad = st.bad;
-        w.parts[at] = out;
+    PartOut out = {st.sum, st.top, kNoBound, st.finite, st.bad, 0};
+#pragma unroll 1
+    for (int rank = w.rank; rank > 0; rank /= 4) {      // (a smaller one where the list is full)
+        const uint32_t bound = list_bound(st.own_top, rank, keys);
+        const int n = list_stretch<T, NT>(x, value_of(bound), kPlaces, part,
+                                          [&](int i, u64 key) { w.lists[at * kPlaces + i] = key; });
+        if (n <= kPlaces) {
+            out.bound = bound;
+            out.listed = n;
+            break;
+        }
+        __syncthreads();
     }
+    if (threadIdx.x == 0) w.parts[at] = out;
 }
 
-template <int T>
-__global__ __launch_bounds__(1024) void sample_join_kernel(const SampleArgs a, const Work w)
+// INLINE: rows that the list does not answer are read here.
+template <int T, bool INLINE>
+__global__ __launch_bounds__(kPartThreads) void sample_join_kernel(const SampleArgs a, const Work w)
 {
-    constexpr int NT = 1024;
+    constexpr int NT = kPartThreads, kWaves = NT / 64;
     __shared__ Shared<NT> s;
+    __shared__ int ends[NT + 1];
     const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const Settings set(a, row);
+    const int tid = threadIdx.x, wave = wave_uniform(tid >> 6), lane = tid & 63;
     const PartOut *parts = w.parts + row * w.n_parts;
-    PartOut p;
-    p.top = -INFINITY; p.bound = 0; p.finite = 0; p.bad = 0; p.sum = 0.0;
+    PartOut p = {0.0, -INFINITY, 0, 0, 0, 0};           // this thread's first part
     if (tid < w.n_parts) p = parts[tid];
+    const Settings set(a, row);
     if (tid == 0) s.listed = 0;
     Row r;
-    // (the largest of the keys; a row that is all -infinity has the key of that)
-    u64 best = (u64)value_key(p.top) << 32 | p.bound;
-    uint32_t top = (uint32_t)(best >> 32), bound = (uint32_t)best;
+    // (by the keys; a row that is all -infinity has the key of that)
+    uint32_t top = 0, bound = 0;
+    u64 counts = 0;
+    for (int i = tid; i < w.n_parts; i += NT) {
+        const PartOut o = i == tid ? p : parts[i];
+        top = max(top, value_key(o.top));
+        bound = max(bound, o.bound);
+        counts += (u64)o.bad << 32 | o.finite;
+    }
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
         top = max(top, (uint32_t)__shfl_xor((int)top, d));
         bound = max(bound, (uint32_t)__shfl_xor((int)bound, d));
+        counts += __shfl_xor(counts, d);
     }
-    if (lane == 0) s.part[wave] = (u64)top << 32 | bound;
+    if (lane == 0) {
+        s.part[wave] = (u64)top << 32 | bound;
+        s.list[wave] = counts;
+    }
     __syncthreads();
-    for (int i = 0; i < NT / 64; ++i) {
+    counts = 0;
+    for (int i = 0; i < kWaves; ++i) {
         top = max(top, (uint32_t)(s.part[i] >> 32));
         bound = max(bound, (uint32_t)s.part[i]);
+        counts += s.list[i];
     }
     r.top = value_of(top);
     r.bound = bound;
-    const u64 counts = block_sum<NT>((u64)p.bad << 32 | p.finite, s.part);
     r.finite = (uint32_t)counts;
     r.bad = (uint32_t)(counts >> 32);
     r.sum = 0.0;
-    if (set.needs_sum() && !r.bad && r.finite)
-        r.sum = block_sum<NT>(p.sum > 0.0 ? p.sum * exp2_64(((double)p.top - (double)r.top) * set.scale) : 0.0,
-                              s.part);
-    if (r.bound != kNoBound) {
-        const u64 *lists = w.lists + row * w.n_parts * (kPartWaves * kPlaces);
-        for (int l = wave; l < w.n_parts * kPartWaves; l += NT / 64) {
-            const int n = parts[l / kPartWaves].listed[l % kPartWaves];
-            for (int i = lane; i - lane < n; i += 64) {
-                const u64 key = i < n ? lists[l * kPlaces + i] : 0;
-                const bool real = (uint32_t)(key >> 32) >= r.bound && i < n;
-                const u64 in = __ballot(real);
+    if (no_row(a, row, r)) return;
+    __syncthreads();
+    for (int l0 = 0; l0 < w.n_parts && r.bound != kNoBound; l0 += NT) {
+        // NT lists at a time, one after another as one run of logits
+        int end = l0 + tid < w.n_parts ? (l0 == 0 ? p.listed : parts[l0 + tid].listed) : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int c = __shfl_up(end, d);
+            if (lane >= d) end += c;
+        }
+        if (lane == 63) s.wave[wave].count = (uint32_t)end;
+        __syncthreads();
+        for (int i = 0; i < wave; ++i) end += (int)s.wave[i].count;
+        ends[tid + 1] = end;
+        if (tid == 0) ends[0] = 0;
+        __syncthreads();
+        const int n = ends[NT];
+        const u64 *lists = w.lists + (row * w.n_parts + l0) * kPlaces;
+        for (int e0 = 0; e0 < n; e0 += 8 * NT) {
+            u64 key[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int e = e0 + u * NT + tid;
+                key[u] = 0;
+                if (e0 + u * NT < n && e < n) {
+                    int l = 0;                          // the last list that begins at e or before
+#pragma unroll
+                    for (int d = NT / 2; d; d >>= 1)
+                        if (ends[l + d] <= e) l += d;
+                    key[u] = lists[(int64_t)l * kPlaces + (e - ends[l])];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (e0 + u * NT >= n) break;
+                const bool in = (uint32_t)(key[u] >> 32) >= r.bound;         // (a bound is not 0)
+                const uint64_t some = __ballot(in);
+                if (!some) continue;
                 int at = 0;
-                if (lane == 0) at = atomicAdd(&s.listed, (int)__popcll(in));
-                at = wave_uniform(at) + __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32),
-                                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
-                if (real && at < Shared<NT>::kList) s.list[at] = key;
+                if (lane == 0) at = atomicAdd(&s.listed, (int)__popcll(some));
+                at = wave_uniform(at) + __builtin_amdgcn_mbcnt_hi((uint32_t)(some >> 32),
+                                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)some, 0));
+                if (in && at < kRowList) s.list[at] = key[u];
             }
         }
+        __syncthreads();
+    }
+    if (set.sum() != Settings::kNone) {
+        double sum = 0.0;
+        for (int i = tid; i < w.n_parts; i += NT) {
+            const double some = i == tid ? p.sum : parts[i].sum;
+            const float beside = i == tid ? p.top : parts[i].top;
+            if (some > 0.0) sum += some * exp2_64(((double)beside - (double)r.top) * set.scale);
+        }
+        r.sum = block_sum<NT>(sum, s.part);
     }
     __syncthreads();
     r.listed = s.listed;
-    row_answers<T, NT>(a, row, set, r, s);
-}
-
-// Rows of up to 65536 logits are held whole; longer ones in parts.
-constexpr int kPartLogits = 16384;
-
-int64_t n_parts(int64_t n_vocab)
-{
-    return n_vocab <= 65536 ? 0 : (n_vocab + kPartLogits - 1) / kPartLogits;
-}
-
-constexpr int64_t kPartBytes = sizeof(PartOut) + sizeof(u64) * kPartWaves * kPlaces;
-
-template <int T, int NT, int E>
-int launch_row(const SampleArgs &a, hipStream_t stream)
-{
-    // (2^32 threads bound a launch)
-    constexpr int64_t most = (int64_t)1 << 21;
-    for (int64_t i = 0; i < a.m; i += most) {
-        SampleArgs b = a;
-        b.m = a.m - i < most ? a.m - i : most;
-        b.logits = (const uint8_t *)a.logits + i * a.row_stride * (T == Q8_T_F32 ? 4 : 2);
-        b.u += i; b.ids += i; b.logprob += i; b.kept += i;
-        if (b.temperature) b.temperature += i;
-        if (b.top_k) b.top_k += i;
-        if (b.top_p) b.top_p += i;
-        if (b.min_p) b.min_p += i;
-        hipLaunchKernelGGL((sample_row_kernel<T, NT, E>), dim3((unsigned)b.m), dim3(NT), 0, stream, b);
-        if (hipGetLastError() != hipSuccess) return -6;
+    Listed<NT> l;
+    const bool listed = r.listed > 0 && r.listed <= kRowList;
+    l.take(s, listed ? r.listed : 0);
+    if (listed && from_list<NT>(a, row, set, r, s, l)) return;
+    __syncthreads();
+    if (!listed) {
+        r.bound = kNoBound;
+        r.listed = 0;
     }
-    return 0;
+    if constexpr (INLINE)
+        from_row<T, NT>(a, row, set, r, s, l, r.bound);
+    else {
+        if (tid == 0) s.index = atomicAdd(w.n_again, 1);
+        __syncthreads();
+        Again &g = w.again[s.index];
+        for (int i = tid; i < kRowBins; i += NT) {
+            g.mass[i] = 0;
+            g.count[i] = 0;
+        }
+        for (int i = 0; i < Listed<NT>::N; ++i) g.list[tid + i * NT] = l.key[i];
+        if (tid == 0) {
+            g.least_mass = 0;
+            g.least_count = 0;
+            g.row = (int)row;
+            g.r = r;
+        }
+    }
 }
+
+constexpr int kAgainGroups = 1024;
+
+// Histograms of the rows that are read again, by parts.
+template <int T>
+__global__ __launch_bounds__(256) void sample_bins_kernel(const SampleArgs a, const Work w)
+{
+    typedef typename Elem<T>::type E;
+    constexpr int NT = 256, V = kVec<T>;
+    __shared__ uint32_t count[kRowBins];
+    __shared__ u64 mass[kRowBins];
+    __shared__ u64 part[NT / 64];
+    const int tid = threadIdx.x;
+    const int64_t items = (int64_t)*w.n_again * w.n_parts;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        Again &g = w.again[item / w.n_parts];
+        const int64_t row = g.row;
+        const int first = (int)(item % w.n_parts) * w.part_len, len = min(w.part_len, (int)a.n_vocab - first);
+        const Settings set(a, row);
+        if (set.greedy) continue;
+        const Row r = g.r;
+        const Weights weights(r.top, set.scale, units_sum(set, r));
+        for (int i = tid; i < kRowBins; i += NT) {
+            count[i] = 0;
+            mass[i] = 0;
+        }
+        __syncthreads();
+        RowBins<kRowBins> bins(weights, set.least);
+        const E *x = (const E *)a.logits + row * a.row_stride + first;
+        const int vecs = len / V;
+        for (int v = tid; v < vecs; v += NT) {
+            float y[V];
+            unpack16<T>(*(const u32x4_any *)(x + v * V), y);
+#pragma unroll
+            for (int j = 0; j < V; ++j) bins.add(y[j], count, mass);
+        }
+        if (vecs * V + tid < len) bins.add((float)x[vecs * V + tid], count, mass);
+        const u64 least_count = block_sum<NT>((u64)bins.kept.count, part);
+        const u64 least_mass = block_sum<NT>(bins.kept.mass, part);
+        // (whole numbers: the order of the sums does not matter)
+        for (int i = tid; i < kRowBins; i += NT)
+            if (count[i]) {
+                atomicAdd(&g.count[i], count[i]);
+                atomicAdd(&g.mass[i], mass[i]);
+            }
+        if (tid == 0) {
+            atomicAdd(&g.least_count, (uint32_t)least_count);
+            atomicAdd(&g.least_mass, least_mass);
+        }
+        __syncthreads();
+    }
+}
+
+// Their answers.
+template <int T>
+__global__ __launch_bounds__(1024) void sample_again_kernel(const SampleArgs a, const Work w)
+{
+    constexpr int NT = 1024;
+    __shared__ Shared<NT> s;
+    const int tid = threadIdx.x, n = *w.n_again;
+    for (int item = blockIdx.x; item < n; item += gridDim.x) {
+        const Again &g = w.again[item];
+        const int64_t row = g.row;
+        const Settings set(a, row);
+        const Row r = g.r;
+        __syncthreads();
+        if (set.greedy) {
+            const int i = nth_equal<T, NT>(a, row, value_key(r.top), 1, s);
+            if (tid == 0) greedy_answer(a, row, i);
+            continue;
+        }
+        for (int i = tid; i < kRowBins; i += NT) {
+            s.first_count[i] = g.count[i];
+            s.first_mass[i] = g.mass[i];
+        }
+        Listed<NT> l;
+#pragma unroll
+        for (int i = 0; i < Listed<NT>::N; ++i) l.key[i] = i < kRowList / NT ? g.list[tid + i * NT] : 0;
+        const Weights weights(r.top, set.scale, units_sum(set, r));
+        __syncthreads();
+        from_bins<T, NT>(a, row, set, r.finite, weights, {g.least_count, g.least_mass}, s, l, r.bound);
+    }
+}
+
+constexpr int kShortRow = 4096;      // logits of a row that one workgroup of 256 takes
+constexpr int64_t kInline = 1 << 18; // calls of up to so many logits read rows again in their join
+constexpr int kGroupRows = 2048;     // rows that share a workspace's turn
+
+template <int T>
+constexpr int kPartMost = Held<T, kPartThreads>::kLogits;
+
+// Parts of a row: as few as there can be where rows are many, and as many as
+// give each CU two where they are few, of 2048 logits or more.
+int64_t n_parts(int64_t m, int64_t n_vocab, int64_t most)
+{
+    const int64_t few = (n_vocab + most - 1) / most, many = n_vocab / 2048;
+    const int64_t wanted = (512 + m - 1) / m;
+    return wanted < few ? few : wanted > many ? (many > few ? many : few) : wanted;
+}
+
+constexpr int64_t kPartBytes = sizeof(PartOut) + sizeof(u64) * kPlaces;
+
+SampleArgs rows_of(const SampleArgs &a, int64_t from, int64_t most)
+{
+    SampleArgs b = a;
+    b.m = a.m - from < most ? a.m - from : most;
+    b.logits = (const uint8_t *)a.logits + from * a.row_stride * (a.type == Q8_T_F32 ? 4 : 2);
+    b.u += from; b.ids += from; b.logprob += from; b.kept += from;
+    if (b.temperature) b.temperature += from;
+    if (b.top_k) b.top_k += from;
+    if (b.top_p) b.top_p += from;
+    if (b.min_p) b.min_p += from;
+    return b;
+}
+
+bool launched() { return hipGetLastError() == hipSuccess; }
 
 template <int T>
 int launch_parts(const SampleArgs &a, void *ws, hipStream_t stream)
 {
-    const int64_t parts = n_parts(a.n_vocab);
-    // (65535 rows bound a grid's second dimension)
-    constexpr int64_t most = 65535;
-    for (int64_t i = 0; i < a.m; i += most) {
-        SampleArgs b = a;
-        b.m = a.m - i < most ? a.m - i : most;
-        b.logits = (const uint8_t *)a.logits + i * a.row_stride * (T == Q8_T_F32 ? 4 : 2);
-        b.u += i; b.ids += i; b.logprob += i; b.kept += i;
-        if (b.temperature) b.temperature += i;
-        if (b.top_k) b.top_k += i;
-        if (b.top_p) b.top_p += i;
-        if (b.min_p) b.min_p += i;
+    for (int64_t i = 0; i < a.m; i += kGroupRows) {
+        const SampleArgs b = rows_of(a, i, kGroupRows);
+        const int64_t parts = n_parts(b.m, a.n_vocab, kPartMost<T>);
+        const bool again = a.m * a.n_vocab > kInline;
         Work w;
-        w.lists = (u64 *)ws;
-        w.parts = (PartOut *)(w.lists + b.m * parts * (kPartWaves * kPlaces));
+        w.n_again = (int *)ws;
+        w.lists = (u64 *)((uint8_t *)ws + 256);
+        w.parts = (PartOut *)(w.lists + b.m * parts * kPlaces);
+        w.again = (Again *)(w.parts + b.m * parts);
         w.n_parts = (int)parts;
-        const int64_t rank = 2048 / parts;
-        w.rank = (int)(rank < 32 ? 32 : rank > 128 ? 128 : rank);
-        hipLaunchKernelGGL((sample_part_kernel<T, kPartLogits / kPartThreads>), dim3((unsigned)parts, (unsigned)b.m),
-                           dim3(kPartThreads), 0, stream, b, w);
-        if (hipGetLastError() != hipSuccess) return -6;
-        hipLaunchKernelGGL((sample_join_kernel<T>), dim3((unsigned)b.m), dim3(1024), 0, stream, b, w);
-        if (hipGetLastError() != hipSuccess) return -6;
+        w.part_len = (int)((a.n_vocab + 8 * parts - 1) / (8 * parts) * 8);
+        w.rank = parts > 64 ? 16 : parts > 8 ? 1024 / (int)parts : kRank;
+        hipLaunchKernelGGL((sample_part_kernel<T>), dim3((unsigned)parts, (unsigned)b.m), dim3(kPartThreads), 0,
+                           stream, b, w);
+        if (!launched()) return -6;
+        if (!again) {
+            hipLaunchKernelGGL((sample_join_kernel<T, true>), dim3((unsigned)b.m), dim3(kPartThreads), 0, stream, b,
+                               w);
+            if (!launched()) return -6;
+            continue;
+        }
+        hipLaunchKernelGGL((sample_join_kernel<T, false>), dim3((unsigned)b.m), dim3(kPartThreads), 0, stream, b, w);
+        if (!launched()) return -6;
+        const int64_t items = b.m * parts;
+        hipLaunchKernelGGL((sample_bins_kernel<T>), dim3((unsigned)(items < kAgainGroups ? items : kAgainGroups)),
+                           dim3(256), 0, stream, b, w);
+        if (!launched()) return -6;
+        hipLaunchKernelGGL((sample_again_kernel<T>), dim3((unsigned)(b.m < 256 ? b.m : 256)), dim3(1024), 0,
+                           stream, b, w);
+        if (!launched()) return -6;
     }
     return 0;
 }
@@ -859,20 +1249,28 @@ int launch_parts(const SampleArgs &a, void *ws, hipStream_t stream)
 template <int T>
 int launch_type(const SampleArgs &a, void *ws, hipStream_t stream)
 {
-    if (n_parts(a.n_vocab)) return launch_parts<T>(a, ws, stream);
-    if (a.n_vocab <= 4096) return launch_row<T, 256, 16>(a, stream);
-    if (a.n_vocab <= 16384) return launch_row<T, 1024, 16>(a, stream);
-    if (a.n_vocab <= 32768) return launch_row<T, 1024, 32>(a, stream);
-    return launch_row<T, 1024, 64>(a, stream);
+    if (a.n_vocab > kShortRow) return launch_parts<T>(a, ws, stream);
+    // (2^32 threads bound a launch)
+    constexpr int64_t most = (int64_t)1 << 23;
+    for (int64_t i = 0; i < a.m; i += most) {
+        const SampleArgs b = rows_of(a, i, most);
+        hipLaunchKernelGGL((sample_row_kernel<T>), dim3((unsigned)b.m), dim3(kPartThreads), 0, stream, b);
+        if (!launched()) return -6;
+    }
+    return 0;
 }
 
 }  // namespace
 
+// Enough for any call of up to m rows of up to n_vocab logits, of any type.
 size_t sample_ws_bytes(int64_t m, int64_t n_vocab)
 {
-    const int64_t rows = m < 65535 ? m : 65535, parts = n_parts(n_vocab);
-    const int64_t b = rows * parts * kPartBytes;
-    return (size_t)(b > 256 ? b : 256);
+    if (n_vocab <= kShortRow || m == 0) return 256;
+    const int64_t rows = m < kGroupRows ? m : kGroupRows;
+    // fewer rows take more parts, 512 together and one more each
+    int64_t parts = rows * ((n_vocab + kPartMost<Q8_T_F32> - 1) / kPartMost<Q8_T_F32>);
+    if (parts < 512 + rows) parts = 512 + rows;
+    return 256 + (size_t)(parts * kPartBytes + rows * (int64_t)sizeof(Again));
 }
 
 int launch_sample(const SampleArgs &a, void *ws, hipStream_t stream)

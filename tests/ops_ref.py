@@ -92,7 +92,7 @@ def sample_row(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     """One row (fp64 values of the logits) by sorting it: a dict with the order,
     the range of sizes of what is kept, the range of places of the drawn token,
     and the log probability of a place.  The library sums whole units of
-    2^-52, or of 2^-60 of the sum at most: targets are met within n of them, and where that much
+    2^-52, or of 2^-60 of the sum (of n where no sum is taken): targets are met within n of them, and where that much
     decides, either side may come out."""
     if np.isnan(x).any() or np.isposinf(x).any():
         return {"id": -1, "kept": 0, "logprob": np.nan}
@@ -106,7 +106,8 @@ def sample_row(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     z = (x[order] - x[order[0]]) / float(np.float32(temperature))
     w = np.exp(z.astype(np.longdouble))
     c = np.cumsum(w)
-    slack = n * max(2.0 ** -52, float(c[-1]) * 2.0 ** -60)
+    most = n if top_k > 0 or (min_p > 0 and not top_p < 1) else float(c[-1])
+    slack = n * max(2.0 ** -52, most * 2.0 ** -60)
     whole = bool(np.all(w == 1))          # whole numbers of units: targets are met exactly
 
     def reach(target, strict):
