@@ -36,7 +36,7 @@ typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 typedef unsigned long long u64;
 
 constexpr float kReach = 64.0f;   // a histogram by value covers weights down to 2^-64
-constexpr int kPlaces = 512;      // listed logits of a part
+constexpr int kPlaces = 128;      // listed logits of a part
 constexpr int kRank = 128;        // how many maxima reach a list's bound, of 256: at most
 
 // 2^t for t <= 0 (2^-1000 below -1000), off by 1.5e-14 at most: 2^r on [-1/2, 1/2]
@@ -74,7 +74,7 @@ struct Settings {
     double scale;                 // log2(e) / T; 0: the largest logit
     uint32_t top_k;               // 0: all
     double top_p;                 // 1: all
-    double least;                 // log2(min_p); -infinity: all
+    float min_p;                  // 0: all
     bool greedy;
 
     __device__ __forceinline__ Settings(const SampleArgs &a, int64_t row)
@@ -88,7 +88,12 @@ struct Settings {
         scale = greedy ? 0.0 : 1.4426950408889634074 / (double)temp;
         top_k = k > 0 ? (uint32_t)k : 0u;
         top_p = p < 1.0f ? fmax((double)p, 0.0) : 1.0;
-        least = m > 0.0f ? fmin(log2((double)m), 0.0) : -INFINITY;
+        min_p = m > 0.0f ? m : 0.0f;
+    }
+    // the least distance to the largest logit that min-p keeps, in powers of two
+    __device__ __forceinline__ double least() const
+    {
+        return min_p > 0.0f ? fmin(log2((double)min_p), 0.0) : -INFINITY;
     }
     // The sum of a row's weights: not needed where a head of the order is cut
     // without it; in 32 bits for a share of it; in 64 bits as the mass of a row
@@ -96,16 +101,19 @@ struct Settings {
     enum Sum { kNone, kRough, kFull };
     __device__ __forceinline__ Sum sum() const
     {
-        if (greedy || top_k > 0 || (top_p >= 1.0 && least > -INFINITY)) return kNone;
+        if (greedy || top_k > 0 || (top_p >= 1.0 && min_p > 0.0f)) return kNone;
         return top_p < 1.0 && scale > 1e-30 && scale < 1e30 ? kRough : kFull;
     }
 };
 
 // How far a rough sum may be off, relative: with |t| the distance to the largest
-// logit in powers of two, a term carries 3 2^-24 ln 2 |t| (difference, scale,
-// product) and 2^-23 (the exponential), and the weights' mean of |t| over a part
-// of n logits is below log2(n) <= 14; sums of 8 add 7 2^-24: 2.3e-6 in all.
-constexpr double kRoughError = 0x1p-18;
+// logit in powers of two, a term carries 2 2^-24 ln 2 |t| (the scale, the fused
+// product) and 2^-23 (the exponential); over a part of up to 2^13 logits beside
+// its largest the weights' mean of |t| is below 9 (n - 1 terms at s = 10 make the
+// most of (n - 1) s 2^-s / (1 + (n - 1) 2^-s)); the sums of 8 add 3 2^-24, the
+// rounding of the product with the largest logit, at most 2^-4, taken out by a
+// factor, 2^-23 and 2^-28: 1.2e-6 in all.
+constexpr double kRoughError = 0x1p-19;
 
 // What the weights of a row are formed with.
 struct Weights {
@@ -138,11 +146,11 @@ struct Head {                     // tokens at the head of the order
 
 template <int NT>
 struct __align__(16) Shared {
-    static constexpr int kBins = NT == 1024 ? 2048 : 1024;    // of a histogram of the row
-    static constexpr int kBinBits = NT == 1024 ? 11 : 10;
-    static constexpr int kList = NT == 1024 ? 4096 : 2048;    // logits of a list
-    static constexpr int kMembers = NT == 1024 ? 512 : 256;   // of one bin of a list
-    static_assert(NT == 1024 || NT == 256, "bins by powers of two");
+    static constexpr int kBins = 4 * NT;               // of a histogram of the row
+    static constexpr int kBinBits = NT == 512 ? 11 : 10;
+    static constexpr int kList = 8 * NT;               // logits of a list
+    static constexpr int kMembers = 2 * NT;            // of one bin of a list
+    static_assert(kBins == 1 << kBinBits, "bins by powers of two");
     union {
         uint32_t keys[256];
         struct {                  // a list, in bins by value
@@ -221,9 +229,11 @@ __device__ __forceinline__ Head scan(Shared<NT> &s, Head before, Head own)
     }
     if (lane == 63) s.wave[wave] = sum;
     __syncthreads();
-    for (int w = 0; w < wave; ++w) {
-        before.count += s.wave[w].count;
-        before.mass += s.wave[w].mass;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        const Head o = s.wave[w];
+        before.count += w < wave ? o.count : 0u;
+        before.mass += w < wave ? o.mass : 0ull;
     }
     return {before.count + sum.count - own.count, before.mass + sum.mass - own.mass};
 }
@@ -404,10 +414,11 @@ struct Listed {
     }
 };
 
-// The row's answers from its list; false where they do not lie in it.
+// The row's answers from its list; false where they do not lie in it.  sum: what
+// r.sum is.
 template <int NT>
-__device__ bool from_list(const SampleArgs &a, int64_t row, const Settings &set, const Row &r, Shared<NT> &s,
-                          Listed<NT> &l)
+__device__ __forceinline__ bool from_list(const SampleArgs &a, int64_t row, const Settings &set, const Row &r,
+                                          Settings::Sum sum, Shared<NT> &s, Listed<NT> &l)
 {
     const int tid = threadIdx.x, n = r.listed;
     const bool all = (uint32_t)n == r.finite, cut = set.top_k > 0 && set.top_k < r.finite;
@@ -426,7 +437,6 @@ __device__ bool from_list(const SampleArgs &a, int64_t row, const Settings &set,
         }
         return true;
     }
-    const Settings::Sum sum = set.sum();
     const float low = value_of(r.bound);
     const Weights w(r.top, set.scale, sum != Settings::kNone ? r.sum : (double)n);
     l.sort(s, w, r.top, low, {0, 0});
@@ -450,8 +460,9 @@ __device__ bool from_list(const SampleArgs &a, int64_t row, const Settings &set,
         }
         if (step == 2) {
             // the tokens that min-p keeps are all listed, or all that is listed is among them
-            if (set.least > -INFINITY && (all || w.t(low) < set.least)) {
-                const Head least = l.least(s, w, set.least);
+            const double reach = set.least();
+            if (set.min_p > 0.0f && (all || w.t(low) < reach)) {
+                const Head least = l.least(s, w, reach);
                 if (least.count < head.count) {
                     head = least;
                     whole = false;
@@ -669,7 +680,7 @@ __device__ __forceinline__ void from_row(const SampleArgs &a, int64_t row, const
         s.first_mass[i] = 0;
     }
     __syncthreads();
-    RowBins<kBins> bins(w, set.least);
+    RowBins<kBins> bins(w, set.least());
     each<T, NT>(a, row, [&](float x, int) { bins.add(x, s.first_count, s.first_mass); });
     Head least;
     least.count = (uint32_t)block_sum<NT>((u64)bins.kept.count, s.part);
@@ -690,24 +701,42 @@ __device__ __forceinline__ bool no_row(const SampleArgs &a, int64_t row, const R
 }
 
 // ---------------------------------------------------------------------------
-// A stretch of a row, 8 vectors of 16 bytes a thread, in LDS, where each thread
+// A stretch of a row, VECS vectors of 16 bytes a thread, in LDS, where each thread
 // keeps its own: loops over them stay rolled and take few registers.  What is
 // left after the last whole vector is one logit a thread.
-constexpr int kVecs = 8;
-
-template <int T, int NT>
+template <int T, int NT, int VECS>
 struct Held {
-    static constexpr int V = kVec<T>, kLogits = kVecs * V * NT;
-    u32x4 *lds;                   // [kVecs][NT]
+    static constexpr int V = kVec<T>, kLogits = VECS * V * NT;
+    u32x4 *lds;                   // [VECS][NT]
+    u32x4 raw[VECS];              // on their way
+    float most[VECS];             // the largest logit of each vector
     float extra;
     int begin, extra_at;          // indices in the row
+
+    // logits first .. first + len - 1 of the row
+    __device__ __forceinline__ void load(const SampleArgs &a, int64_t row, int first, int len)
+    {
+        typedef typename Elem<T>::type El;
+        const uint32_t none = T == Q8_T_F32 ? 0xff800000u : T == Q8_T_F16 ? 0xfc00fc00u : 0xff80ff80u;
+        const El *p = (const El *)a.logits + row * a.row_stride + first;
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+            const int i = (threadIdx.x + v * NT) * V;
+            raw[v] = (u32x4){none, none, none, none};
+            if (i + V <= len) raw[v] = *(const u32x4_any *)(p + i);
+        }
+        const int left = len / V * V + threadIdx.x;
+        begin = first;
+        extra_at = first + left;
+        extra = left < len ? (float)p[left] : -INFINITY;
+    }
 
     // f(value, index); beyond the stretch -infinity
     template <class F>
     __device__ __forceinline__ void each(F f) const
     {
 #pragma unroll 1
-        for (int v = 0; v < kVecs; ++v) {
+        for (int v = 0; v < VECS; ++v) {
             float y[V];
             unpack16<T>(lds[v * NT + threadIdx.x], y);
             const int i = begin + (int)(threadIdx.x + v * NT) * V;
@@ -726,47 +755,34 @@ struct Stretch {
     double sum;
 };
 
-// logits first .. first + len - 1 of the row into x and their statistics
-template <int T, int NT>
-__device__ __forceinline__ Stretch stretch(const SampleArgs &a, int64_t row, int first, int len,
-                                           const Settings &set, Held<T, NT> &x, u64 *part)
+// The logits loaded go to LDS; their statistics.  (The maximum that NaN passes
+// through: one instruction for two logits, without a comparison for NaN.)
+template <int T, int NT, int VECS>
+__device__ __forceinline__ Stretch stretch(const Settings &set, Held<T, NT, VECS> &x, u64 *part)
 {
-    typedef typename Elem<T>::type El;
     constexpr int V = kVec<T>;
-    const uint32_t none = T == Q8_T_F32 ? 0xff800000u : T == Q8_T_F16 ? 0xfc00fc00u : 0xff80ff80u;
-    const El *p = (const El *)a.logits + row * a.row_stride + first;
-    u32x4 raw[kVecs];
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-        const int i = (threadIdx.x + v * NT) * V;
-        raw[v] = (u32x4){none, none, none, none};
-        if (i + V <= len) raw[v] = *(const u32x4_any *)(p + i);
-    }
-    const int left = len / V * V + threadIdx.x;
-    x.begin = first;
-    x.extra_at = first + left;
-    x.extra = left < len ? (float)p[left] : -INFINITY;
-
+    auto larger = [](float p, float q) { return __builtin_elementwise_maximum(p, q); };
     Stretch r = {-INFINITY, x.extra, 0, 0, 0.0};
     float lowest = x.extra;
-    bool bad = x.extra != x.extra;
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
+    for (int v = 0; v < VECS; ++v) {
         float y[V];
-        x.lds[v * NT + threadIdx.x] = raw[v];
-        unpack16<T>(raw[v], y);
+        x.lds[v * NT + threadIdx.x] = x.raw[v];
+        unpack16<T>(x.raw[v], y);
+        x.most[v] = larger(y[0], y[1]);
+        lowest = fminf(fminf(y[0], y[1]), lowest);
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            r.own_top = fmaxf(fmaxf(y[j], y[j + 1]), r.own_top);
+        for (int j = 2; j < V; j += 2) {
+            x.most[v] = larger(larger(y[j], y[j + 1]), x.most[v]);
             lowest = fminf(fminf(y[j], y[j + 1]), lowest);
-            bad |= __builtin_isunordered(y[j], y[j + 1]);
         }
+        r.own_top = larger(r.own_top, x.most[v]);
         __builtin_amdgcn_sched_barrier(0);
     }
-    bad |= r.own_top == INFINITY;
+    const bool bad = !(r.own_top < INFINITY);
     uint32_t finite = 0;
     if (lowest == -INFINITY) x.each([&](float v, int) { finite += v > -INFINITY; });
-    else finite = kVecs * V + 1;
+    else finite = VECS * V + 1;
     r.top = r.own_top;
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
@@ -787,17 +803,24 @@ __device__ __forceinline__ Stretch stretch(const SampleArgs &a, int64_t row, int
     const Settings::Sum kind = set.sum();
     if (kind == Settings::kNone || r.top == -INFINITY || r.bad) return r;
     double sum = 0.0;
-    if (kind == Settings::kRough) {
-        const float scale = (float)set.scale;
+    const float scale = (float)set.scale, off = r.top * scale;
+    if (kind == Settings::kRough && fabsf(off) < 0x1p20f) {
+        // 2^(v scale - off), a fused product each; what off was rounded by is a
+        // factor of the sum
 #pragma unroll 2
-        for (int v = 0; v < kVecs; ++v) {
-            float y[V], some = 0.0f;
+        for (int v = 0; v < VECS; ++v) {
+            float y[V];
             unpack16<T>(x.lds[v * NT + threadIdx.x], y);
 #pragma unroll
-            for (int j = 0; j < V; ++j) some += __builtin_amdgcn_exp2f((y[j] - r.top) * scale);
-            sum += (double)some;
+            for (int j = 0; j < V; ++j) y[j] = __builtin_amdgcn_exp2f(fmaf(y[j], scale, -off));
+#pragma unroll
+            for (int d = 1; d < V; d *= 2)
+#pragma unroll
+                for (int j = 0; j < V; j += 2 * d) y[j] += y[j + d];
+            sum += (double)y[0];
         }
-        sum += (double)__builtin_amdgcn_exp2f((x.extra - r.top) * scale);
+        sum += (double)__builtin_amdgcn_exp2f(fmaf(x.extra, scale, -off));
+        sum *= (double)__builtin_amdgcn_exp2f((float)((double)off - (double)r.top * (double)scale));
     } else {
         // (the difference first: v * scale - top * scale would round masks near the
         // type's lowest value apart)
@@ -808,8 +831,13 @@ __device__ __forceinline__ Stretch stretch(const SampleArgs &a, int64_t row, int
     return r;
 }
 
-// A key that `rank` or more logits of a workgroup of 256 reach: that of the
+// A key that `rank` or more logits of a workgroup of 64 or 256 reach: that of the
 // rank-th of its threads' maxima, its low half cut.
+__device__ __forceinline__ uint32_t list_bound(float own_top, int rank)
+{
+    return max(nth_key(value_key(own_top), rank), kLeastKey);
+}
+
 __device__ __forceinline__ uint32_t list_bound(float own_top, int rank, uint32_t *keys)
 {
     keys[threadIdx.x] = value_key(own_top);
@@ -817,28 +845,52 @@ __device__ __forceinline__ uint32_t list_bound(float own_top, int rank, uint32_t
     return max(nth_key(((const u32x4 *)keys)[threadIdx.x & 63], rank), kLeastKey);
 }
 
-constexpr int kPartThreads = 256;
+constexpr int kJoinThreads = 256;     // of a short row, and of a join
 
 // The logits of a stretch from `low` on as keys to list(place, key), where they
-// are `most` or fewer; returns how many they are.  A thread marks its own in a
-// mask (two instructions a logit), then takes them one by one: few have any.
-template <int T, int NT, class F>
-__device__ __forceinline__ int list_stretch(const Held<T, NT> &x, float low, int most, u64 *part, F list)
+// are `most` or fewer; returns how many they are.  Few vectors have any: the
+// largest logit of each says which.
+template <int T, int NT, int VECS, class F>
+__device__ __forceinline__ int list_stretch(const Held<T, NT, VECS> &x, float low, int most, u64 *part, F list)
 {
-    typedef typename Elem<T>::type El;
     constexpr int V = kVec<T>;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint64_t mask = 0;            // bit V * (kVecs - v) - 1 - j: logit j of vector v
-#pragma unroll 2
-    for (int v = 0; v < kVecs; ++v) {
-        float y[V];
-        unpack16<T>(x.lds[v * NT + threadIdx.x], y);
-        uint32_t m = 0;
+    uint32_t hits = 0;            // a bit per vector
 #pragma unroll
-        for (int j = 0; j < V; ++j) m = m + m + (y[j] >= low);
-        mask = mask << V | m;
+    for (int v = 0; v < VECS; ++v) hits |= x.most[v] >= low ? 1u << v : 0u;
+    if constexpr (NT == 64) {     // by ballots, the lanes' next vectors together
+        int n = 0;
+        auto offer = [&](bool in, float y, int i) {
+            const uint64_t all = __ballot(in);
+            if (!all) return;
+            const int to = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32),
+                                                         __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+            if (in && to < most) list(to, order_key(y, (uint32_t)i));
+            n += __popcll(all);
+        };
+        for (; __ballot(hits != 0); hits &= hits - 1) {
+            const int v = hits ? __builtin_ctz(hits) : 0, i = x.begin + (int)(threadIdx.x + v * NT) * V;
+            float y[V];
+            unpack16<T>(x.lds[v * NT + threadIdx.x], y);
+#pragma unroll
+            for (int j = 0; j < V; ++j) offer(hits != 0 && y[j] >= low, y[j], i + j);
+        }
+        offer(x.extra >= low, x.extra, x.extra_at);
+        return n;
     }
-    int at = __popcll(mask) + (x.extra >= low);
+    auto each_hit = [&](auto f) {
+        for (uint32_t h = hits; h; h &= h - 1) {
+            const int v = __builtin_ctz(h), i = x.begin + (int)(threadIdx.x + v * NT) * V;
+            float y[V];
+            unpack16<T>(x.lds[v * NT + threadIdx.x], y);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (y[j] >= low) f(y[j], i + j);
+        }
+        if (x.extra >= low) f(x.extra, x.extra_at);
+    };
+    int at = 0;
+    each_hit([&](float, int) { ++at; });
     const int mine = at;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -855,37 +907,33 @@ __device__ __forceinline__ int list_stretch(const Held<T, NT> &x, float low, int
         all += (int)part[w];
     }
     __syncthreads();
-    if (all > most) return all;
-    while (mask) {
-        const int bit = __builtin_ctzll(mask), from = kVecs * V - 1 - bit, v = from / V, j = from % V;
-        mask &= mask - 1;
-        const float y = (float)((const El *)(x.lds + v * NT + threadIdx.x))[j];
-        list(at++, order_key(y, (uint32_t)(x.begin + (int)(threadIdx.x + v * NT) * V + j)));
-    }
-    if (x.extra >= low) list(at, order_key(x.extra, (uint32_t)x.extra_at));
+    if (all <= most) each_hit([&](float y, int i) { list(at++, order_key(y, (uint32_t)i)); });
     return all;
 }
 
 // ---------------------------------------------------------------------------
 // Short rows: one per workgroup.
+constexpr int kShortVecs = 4;
+
 template <int T>
-__global__ __launch_bounds__(kPartThreads) void sample_row_kernel(const SampleArgs a)
+__global__ __launch_bounds__(kJoinThreads) void sample_row_kernel(const SampleArgs a)
 {
-    constexpr int NT = kPartThreads;
+    constexpr int NT = kJoinThreads;
     __shared__ Shared<NT> s;
-    __shared__ u32x4 held[kVecs * NT];
+    __shared__ u32x4 held[kShortVecs * NT];
     const int64_t row = blockIdx.x;
     const Settings set(a, row);
-    Held<T, NT> x;
+    Held<T, NT, kShortVecs> x;
     x.lds = held;
-    const Stretch st = stretch<T, NT>(a, row, 0, (int)a.n_vocab, set, x, s.part);
+    x.load(a, row, 0, (int)a.n_vocab);
+    const Stretch st = stretch<T, NT, kShortVecs>(set, x, s.part);
     Row r = {st.top, st.finite, st.bad, st.sum, 0, 0};
     if (no_row(a, row, r)) return;
 #pragma unroll 1
     for (int rank = kRank; rank > 0; rank /= 4) {       // (a smaller one where the list is full)
         r.bound = list_bound(st.own_top, rank, s.keys);
         __syncthreads();          // (the list lies where the keys were)
-        r.listed = list_stretch<T, NT>(x, value_of(r.bound), Shared<NT>::kList, s.part,
+        r.listed = list_stretch<T, NT, kShortVecs>(x, value_of(r.bound), Shared<NT>::kList, s.part,
                                        [&](int at, u64 key) { s.list[at] = key; });
         if (r.listed <= Shared<NT>::kList) break;
         __syncthreads();
@@ -894,7 +942,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_row_kernel(const SampleAr
     Listed<NT> l;
     const bool listed = r.listed > 0 && r.listed <= Shared<NT>::kList;
     l.take(s, listed ? r.listed : 0);
-    if (listed && from_list<NT>(a, row, set, r, s, l)) return;
+    if (listed && from_list<NT>(a, row, set, r, set.sum(), s, l)) return;
     __syncthreads();
     if (!listed) r.bound = kNoBound;
     from_row<T, NT>(a, row, set, r, s, l, r.bound);
@@ -911,11 +959,12 @@ struct PartOut {
     int listed;
 };
 
-constexpr int kRowBins = Shared<1024>::kBins, kRowList = Shared<kPartThreads>::kList;
+constexpr int kAgainThreads = 512;
+constexpr int kRowBins = Shared<kAgainThreads>::kBins, kRowList = Shared<kJoinThreads>::kList;
 
 // A row that is read again.
 struct Again {
-    u64 mass[kRowBins], list[kRowList], least_mass;
+    u64 mass[kRowBins], list[kRowList], least_mass, all_mass;
     uint32_t count[kRowBins], least_count;
     int row;
     Row r;
@@ -929,44 +978,47 @@ struct Work {
     int n_parts, part_len, rank;
 };
 
+// A part is a wave's: what is done once a part (statistics, bound, list) is 350
+// instructions a wave, without barriers, against 17 a logit.
+constexpr int kPartThreads = 64, kPartVecs = 8;
+
 template <int T>
 __global__ __launch_bounds__(kPartThreads) void sample_part_kernel(const SampleArgs a, const Work w)
 {
     constexpr int NT = kPartThreads;
-    __shared__ u32x4 held[kVecs * NT];
+    __shared__ u32x4 held[kPartVecs * NT];
     __shared__ u64 part[NT / 64];
-    __shared__ __align__(16) uint32_t keys[NT];
-    const int64_t row = blockIdx.y;
-    const int first = blockIdx.x * w.part_len, len = min(w.part_len, (int)a.n_vocab - first);
-    if (row == 0 && first == 0 && threadIdx.x == 0) *w.n_again = 0;
-    const Settings set(a, row);
-    Held<T, NT> x;
+    const int64_t row = blockIdx.y, at = row * w.n_parts + blockIdx.x;
+    const int first = blockIdx.x * w.part_len;
+    if (at == 0 && threadIdx.x == 0) *w.n_again = 0;
+    Held<T, NT, kPartVecs> x;
     x.lds = held;
-    const Stretch st = stretch<T, NT>(a, row, first, len, set, x, part);
-    const int64_t at = row * w.n_parts + blockIdx.x;
+    x.load(a, row, first, min(w.part_len, (int)a.n_vocab - first));
+    const Settings set(a, row);
+    const Stretch st = stretch<T, NT, kPartVecs>(set, x, part);
     PartOut out = {st.sum, st.top, kNoBound, st.finite, st.bad, 0};
 #pragma unroll 1
     for (int rank = w.rank; rank > 0; rank /= 4) {      // (a smaller one where the list is full)
-        const uint32_t bound = list_bound(st.own_top, rank, keys);
-        const int n = list_stretch<T, NT>(x, value_of(bound), kPlaces, part,
-                                          [&](int i, u64 key) { w.lists[at * kPlaces + i] = key; });
+        const uint32_t bound = list_bound(st.own_top, rank);
+        const int n = list_stretch<T, NT, kPartVecs>(x, value_of(bound), kPlaces, part,
+                                                     [&](int i, u64 key) { w.lists[at * kPlaces + i] = key; });
         if (n <= kPlaces) {
             out.bound = bound;
             out.listed = n;
             break;
         }
-        __syncthreads();
     }
     if (threadIdx.x == 0) w.parts[at] = out;
 }
 
 // INLINE: rows that the list does not answer are read here.
 template <int T, bool INLINE>
-__global__ __launch_bounds__(kPartThreads) void sample_join_kernel(const SampleArgs a, const Work w)
+__global__ __launch_bounds__(kJoinThreads) void sample_join_kernel(const SampleArgs a, const Work w)
 {
-    constexpr int NT = kPartThreads, kWaves = NT / 64;
+    constexpr int NT = kJoinThreads, kWaves = NT / 64, kRound = 5;
     __shared__ Shared<NT> s;
     __shared__ int ends[NT + 1];
+    const int half = w.n_parts > 1 ? 1 << (31 - __clz(min(w.n_parts, NT) - 1)) : 1;     // of a power of two of parts
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, wave = wave_uniform(tid >> 6), lane = tid & 63;
     const PartOut *parts = w.parts + row * w.n_parts;
@@ -1018,37 +1070,44 @@ __global__ __launch_bounds__(kPartThreads) void sample_join_kernel(const SampleA
         }
         if (lane == 63) s.wave[wave].count = (uint32_t)end;
         __syncthreads();
-        for (int i = 0; i < wave; ++i) end += (int)s.wave[i].count;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) end += i < wave ? (int)s.wave[i].count : 0;
         ends[tid + 1] = end;
         if (tid == 0) ends[0] = 0;
         __syncthreads();
         const int n = ends[NT];
         const u64 *lists = w.lists + (row * w.n_parts + l0) * kPlaces;
-        for (int e0 = 0; e0 < n; e0 += 8 * NT) {
-            u64 key[8];
+        for (int e0 = 0; e0 < n; e0 += kRound * NT) {
+            // the last list that begins at e or before, for each of a thread's places
+            int l[kRound];
+            u64 key[kRound];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int e = e0 + u * NT + tid;
-                key[u] = 0;
-                if (e0 + u * NT < n && e < n) {
-                    int l = 0;                          // the last list that begins at e or before
+            for (int u = 0; u < kRound; ++u) l[u] = 0;
+#pragma unroll 1
+            for (int d = l0 + NT < w.n_parts ? NT / 2 : half; d; d >>= 1)
 #pragma unroll
-                    for (int d = NT / 2; d; d >>= 1)
-                        if (ends[l + d] <= e) l += d;
-                    key[u] = lists[(int64_t)l * kPlaces + (e - ends[l])];
-                }
+                for (int u = 0; u < kRound; ++u) l[u] += ends[l[u] + d] <= min(e0 + u * NT + tid, n - 1) ? d : 0;
+            // (all lanes load, so that no branch keeps one load from the next)
+#pragma unroll
+            for (int u = 0; u < kRound; ++u) {
+                key[u] = lists[(int64_t)l[u] * kPlaces + min(e0 + u * NT + tid, n - 1) - ends[l[u]]];
             }
+            int some = 0, at = 0;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (e0 + u * NT >= n) break;
-                const bool in = (uint32_t)(key[u] >> 32) >= r.bound;         // (a bound is not 0)
-                const uint64_t some = __ballot(in);
-                if (!some) continue;
-                int at = 0;
-                if (lane == 0) at = atomicAdd(&s.listed, (int)__popcll(some));
-                at = wave_uniform(at) + __builtin_amdgcn_mbcnt_hi((uint32_t)(some >> 32),
-                                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)some, 0));
-                if (in && at < kRowList) s.list[at] = key[u];
+            for (int u = 0; u < kRound; ++u) {
+                const bool in = e0 + u * NT + tid < n && (uint32_t)(key[u] >> 32) >= r.bound;
+                key[u] = in ? key[u] : 0;
+                some += __popcll(__ballot(in));
+            }
+            if (lane == 0) at = atomicAdd(&s.listed, some);
+            at = wave_uniform(at);
+#pragma unroll
+            for (int u = 0; u < kRound; ++u) {
+                const uint64_t all = __ballot(key[u] != 0);
+                const int to = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32),
+                                                              __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+                if (key[u] != 0 && to < kRowList) s.list[to] = key[u];
+                at += __popcll(all);
             }
         }
         __syncthreads();
@@ -1067,7 +1126,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_join_kernel(const SampleA
     Listed<NT> l;
     const bool listed = r.listed > 0 && r.listed <= kRowList;
     l.take(s, listed ? r.listed : 0);
-    if (listed && from_list<NT>(a, row, set, r, s, l)) return;
+    if (listed && from_list<NT>(a, row, set, r, set.sum(), s, l)) return;
     __syncthreads();
     if (!listed) {
         r.bound = kNoBound;
@@ -1086,6 +1145,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_join_kernel(const SampleA
         for (int i = 0; i < Listed<NT>::N; ++i) g.list[tid + i * NT] = l.key[i];
         if (tid == 0) {
             g.least_mass = 0;
+            g.all_mass = 0;
             g.least_count = 0;
             g.row = (int)row;
             g.r = r;
@@ -1093,7 +1153,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_join_kernel(const SampleA
     }
 }
 
-constexpr int kAgainGroups = 1024;
+constexpr int kAgainGroups = 1024, kAgainLogits = 4096;
 
 // Histograms of the rows that are read again, by parts.
 template <int T>
@@ -1105,11 +1165,12 @@ __global__ __launch_bounds__(256) void sample_bins_kernel(const SampleArgs a, co
     __shared__ u64 mass[kRowBins];
     __shared__ u64 part[NT / 64];
     const int tid = threadIdx.x;
-    const int64_t items = (int64_t)*w.n_again * w.n_parts;
+    const int per_row = ((int)a.n_vocab + kAgainLogits - 1) / kAgainLogits;
+    const int64_t items = (int64_t)*w.n_again * per_row;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        Again &g = w.again[item / w.n_parts];
+        Again &g = w.again[item / per_row];
         const int64_t row = g.row;
-        const int first = (int)(item % w.n_parts) * w.part_len, len = min(w.part_len, (int)a.n_vocab - first);
+        const int first = (int)(item % per_row) * kAgainLogits, len = min(kAgainLogits, (int)a.n_vocab - first);
         const Settings set(a, row);
         if (set.greedy) continue;
         const Row r = g.r;
@@ -1119,7 +1180,7 @@ __global__ __launch_bounds__(256) void sample_bins_kernel(const SampleArgs a, co
             mass[i] = 0;
         }
         __syncthreads();
-        RowBins<kRowBins> bins(weights, set.least);
+        RowBins<kRowBins> bins(weights, set.least());
         const E *x = (const E *)a.logits + row * a.row_stride + first;
         const int vecs = len / V;
         for (int v = tid; v < vecs; v += NT) {
@@ -1132,14 +1193,18 @@ __global__ __launch_bounds__(256) void sample_bins_kernel(const SampleArgs a, co
         const u64 least_count = block_sum<NT>((u64)bins.kept.count, part);
         const u64 least_mass = block_sum<NT>(bins.kept.mass, part);
         // (whole numbers: the order of the sums does not matter)
+        u64 all = 0;
         for (int i = tid; i < kRowBins; i += NT)
             if (count[i]) {
                 atomicAdd(&g.count[i], count[i]);
                 atomicAdd(&g.mass[i], mass[i]);
+                all += mass[i];
             }
+        all = block_sum<NT>(all, part);
         if (tid == 0) {
             atomicAdd(&g.least_count, (uint32_t)least_count);
             atomicAdd(&g.least_mass, least_mass);
+            atomicAdd(&g.all_mass, all);
         }
         __syncthreads();
     }
@@ -1147,9 +1212,9 @@ __global__ __launch_bounds__(256) void sample_bins_kernel(const SampleArgs a, co
 
 // Their answers.
 template <int T>
-__global__ __launch_bounds__(1024) void sample_again_kernel(const SampleArgs a, const Work w)
+__global__ __launch_bounds__(kAgainThreads) void sample_again_kernel(const SampleArgs a, const Work w)
 {
-    constexpr int NT = 1024;
+    constexpr int NT = kAgainThreads;
     __shared__ Shared<NT> s;
     const int tid = threadIdx.x, n = *w.n_again;
     for (int item = blockIdx.x; item < n; item += gridDim.x) {
@@ -1163,25 +1228,31 @@ __global__ __launch_bounds__(1024) void sample_again_kernel(const SampleArgs a, 
             if (tid == 0) greedy_answer(a, row, i);
             continue;
         }
-        for (int i = tid; i < kRowBins; i += NT) {
-            s.first_count[i] = g.count[i];
-            s.first_mass[i] = g.mass[i];
-        }
         Listed<NT> l;
 #pragma unroll
         for (int i = 0; i < Listed<NT>::N; ++i) l.key[i] = i < kRowList / NT ? g.list[tid + i * NT] : 0;
         const Weights weights(r.top, set.scale, units_sum(set, r));
+        if (r.listed && set.sum() == Settings::kRough) {
+            Row known = r;                     // the list again, with the sum as it is
+            known.sum = (double)g.all_mass * __builtin_amdgcn_ldexp(1.0, -weights.bits);
+            if (from_list<NT>(a, row, set, known, Settings::kFull, s, l)) continue;
+            __syncthreads();
+        }
+        for (int i = tid; i < kRowBins; i += NT) {
+            s.first_count[i] = g.count[i];
+            s.first_mass[i] = g.mass[i];
+        }
         __syncthreads();
         from_bins<T, NT>(a, row, set, r.finite, weights, {g.least_count, g.least_mass}, s, l, r.bound);
     }
 }
 
-constexpr int kShortRow = 4096;      // logits of a row that one workgroup of 256 takes
+constexpr int kShortRow = Held<Q8_T_F32, kJoinThreads, kShortVecs>::kLogits;   // logits of a row that one workgroup takes
 constexpr int64_t kInline = 1 << 18; // calls of up to so many logits read rows again in their join
 constexpr int kGroupRows = 2048;     // rows that share a workspace's turn
 
 template <int T>
-constexpr int kPartMost = Held<T, kPartThreads>::kLogits;
+constexpr int kPartMost = Held<T, kPartThreads, kPartVecs>::kLogits;
 
 // Parts of a row: as few as there can be where rows are many, and as many as
 // give each CU two where they are few, of 2048 logits or more.
@@ -1223,23 +1294,22 @@ int launch_parts(const SampleArgs &a, void *ws, hipStream_t stream)
         w.again = (Again *)(w.parts + b.m * parts);
         w.n_parts = (int)parts;
         w.part_len = (int)((a.n_vocab + 8 * parts - 1) / (8 * parts) * 8);
-        w.rank = parts > 64 ? 16 : parts > 8 ? 1024 / (int)parts : kRank;
+        w.rank = parts > 64 ? 12 : parts > 16 ? 768 / (int)parts : 48;
         hipLaunchKernelGGL((sample_part_kernel<T>), dim3((unsigned)parts, (unsigned)b.m), dim3(kPartThreads), 0,
                            stream, b, w);
         if (!launched()) return -6;
         if (!again) {
-            hipLaunchKernelGGL((sample_join_kernel<T, true>), dim3((unsigned)b.m), dim3(kPartThreads), 0, stream, b,
+            hipLaunchKernelGGL((sample_join_kernel<T, true>), dim3((unsigned)b.m), dim3(kJoinThreads), 0, stream, b,
                                w);
             if (!launched()) return -6;
             continue;
         }
-        hipLaunchKernelGGL((sample_join_kernel<T, false>), dim3((unsigned)b.m), dim3(kPartThreads), 0, stream, b, w);
+        hipLaunchKernelGGL((sample_join_kernel<T, false>), dim3((unsigned)b.m), dim3(kJoinThreads), 0, stream, b, w);
         if (!launched()) return -6;
-        const int64_t items = b.m * parts;
-        hipLaunchKernelGGL((sample_bins_kernel<T>), dim3((unsigned)(items < kAgainGroups ? items : kAgainGroups)),
-                           dim3(256), 0, stream, b, w);
+        hipLaunchKernelGGL((sample_bins_kernel<T>), dim3(kAgainGroups), dim3(256), 0, stream, b, w);
         if (!launched()) return -6;
-        hipLaunchKernelGGL((sample_again_kernel<T>), dim3((unsigned)(b.m < 256 ? b.m : 256)), dim3(1024), 0,
+        hipLaunchKernelGGL((sample_again_kernel<T>), dim3((unsigned)(b.m < 256 ? b.m : 256)),
+                           dim3(kAgainThreads), 0,
                            stream, b, w);
         if (!launched()) return -6;
     }
@@ -1254,7 +1324,7 @@ int launch_type(const SampleArgs &a, void *ws, hipStream_t stream)
     constexpr int64_t most = (int64_t)1 << 23;
     for (int64_t i = 0; i < a.m; i += most) {
         const SampleArgs b = rows_of(a, i, most);
-        hipLaunchKernelGGL((sample_row_kernel<T>), dim3((unsigned)b.m), dim3(kPartThreads), 0, stream, b);
+        hipLaunchKernelGGL((sample_row_kernel<T>), dim3((unsigned)b.m), dim3(kJoinThreads), 0, stream, b);
         if (!launched()) return -6;
     }
     return 0;
