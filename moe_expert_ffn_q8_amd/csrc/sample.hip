@@ -380,21 +380,29 @@ struct Listed {
         __syncthreads();
         const int n = s.members;
         if (n > Shared<NT>::kMembers) return false;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (bin[i] == b) {
-                Head ahead = before;
-                for (int j = 0; j < n; ++j)
-                    if (s.member_key[j] > key[i]) {
-                        ++ahead.count;
-                        ahead.mass += s.member_mass[j];
-                    }
-                const Head with = {ahead.count + 1, ahead.mass + mass[i]};
-                if (!reaches(ahead, by_mass, target) && reaches(with, by_mass, target)) {
-                    s.key = key[i];
-                    s.before = with;
+        // eight lanes to a member count what is ahead of it
+        const int sub = threadIdx.x & 7;
+        for (int c = threadIdx.x >> 3; c < n; c += NT / 8) {
+            const u64 k = s.member_key[c];
+            Head ahead = {0, 0};
+            for (int j = sub; j < n; j += 8)
+                if (s.member_key[j] > k) {
+                    ++ahead.count;
+                    ahead.mass += s.member_mass[j];
                 }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) {
+                ahead.count += __shfl_xor(ahead.count, d);
+                ahead.mass += __shfl_xor(ahead.mass, d);
             }
+            ahead.count += before.count;
+            ahead.mass += before.mass;
+            const Head with = {ahead.count + 1, ahead.mass + s.member_mass[c]};
+            if (sub == 0 && !reaches(ahead, by_mass, target) && reaches(with, by_mass, target)) {
+                s.key = k;
+                s.before = with;
+            }
+        }
         __syncthreads();
         return true;
     }
@@ -543,16 +551,19 @@ __device__ __forceinline__ Head locate(const SampleArgs &a, int64_t row, const W
         if (count <= Shared<NT>::kList) {      // its logits as a list
             if (threadIdx.x == 0) s.listed = 0;
             __syncthreads();
-            auto take = [&](float x, u64 key) {
+            const float low = value_of(lo), high = value_of(hi);
+            auto take = [&](float x, int i) {
+                if (!(x >= low && x <= high)) return;
+                const u64 key = order_key(x, (uint32_t)i);
                 if (!inside(x, (uint32_t)(key >> 32))) return;
                 const int at = atomicAdd(&s.listed, 1);
                 if (at < Shared<NT>::kList) s.list[at] = key;
             };
             if (lo >= known_from) {
                 for (int i = 0; i < Listed<NT>::N; ++i)
-                    if (known.key[i]) take(key_value(known.key[i]), known.key[i]);
+                    if (known.key[i]) take(key_value(known.key[i]), key_index(known.key[i]));
             } else
-                each<T, NT>(a, row, [&](float x, int i) { take(x, order_key(x, (uint32_t)i)); });
+                each<T, NT>(a, row, take);
             __syncthreads();
             Listed<NT> l;
             l.take(s, (int)count);
