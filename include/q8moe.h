@@ -726,7 +726,9 @@ int q8_0_embed_rows(const void *w, int r8, const int32_t *tokens, float scale, v
 /* norm_rows -- y = norm(x) * weight + bias for m rows of n values:
  *   layer 0:      norm(x) = x / sqrt(mean(x^2) + eps)
  *   layer not 0:  norm(x) = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
- * computed in 64 bits and rounded to fp32, then to y's type.
+ * rounded to fp32, then to y's type.  Computed in 64 bits where a row is fp32 or
+ * y is codes, in 32 bits (with sums over threads in 64) where all rows are of
+ * 16-bit types.
  *   x        float rows [m][x_row_stride], aligned to the element
  *   weight   fp32 [n];  bias  fp32 [n], or NULL
  *   y        y_type Q8_T_F32, Q8_T_F16, Q8_T_BF16: rows aligned to the element;
@@ -738,8 +740,8 @@ int q8_0_embed_rows(const void *w, int r8, const int32_t *tokens, float scale, v
  * block's norm:
  *   a             = x, or norm(x) * post_weight + post_bias where post_weight is
  *                   given (post_bias may be NULL)
- *   residual_out  = gate * a + residual_scale * residual, in 64 bits, rounded to
- *                   fp32, then to residual_type
+ *   residual_out  = gate * a + residual_scale * residual, rounded to fp32, then to
+ *                   residual_type
  *   y             = norm(residual_out) * weight + bias, of the values as stored
  *   residual      residual_type rows; residual_out the same type, may be
  *                 residual itself with its stride (in place)

@@ -6,12 +6,19 @@
 //   y  = round(norm(r') * weight + bias), or codes of the fp32 y by the row rule
 //   norm(v) = (v - mean) / sqrt(var + eps), or v / sqrt(mean of v^2 + eps)
 //
-// Everything between the roundings is in 64 bits: fp64 multiply-adds issue at
-// the rate of fp32 ones here and HBM bounds the kernel, and a code of the row
-// rule, which turns at a border, then does not hang on the order of a sum.
+// Two arithmetics.  Where any row is fp32 or codes come out, everything between the
+// roundings is in 64 bits: a code of the row rule turns at a border, and then
+// does not hang on the order of a sum.  Where all rows are 16-bit floats it is
+// in 32 bits, with sums over threads in 64: conversions to and from 64 bits
+// issue at a quarter of the rate of other instructions and would bound the kernel
+// (16384 x 4096 bfloat16 181 us).  There a mean is taken of differences from a
+// thread's first value, so that a row far from 0 loses nothing.
 //
-// A row lies in the registers of one wave or workgroup, 8 values a piece, so
-// every tensor is read and written once.
+// HBM bounds it: a row lies in the registers of one wave or workgroup, 8 values a
+// piece, so every tensor is read and written once; where rows are many a
+// workgroup takes several and keeps the weights.
+#include <type_traits>
+
 #include "i8_device.h"
 #include "q8_ops.h"
 
@@ -66,9 +73,9 @@ __device__ __forceinline__ void store8(void *row, int type, int64_t i, int left,
         store16<Q8_T_F32, false>(p, pack_vec<Q8_T_F32>(lo), left);
         if (left > 4) store16<Q8_T_F32, false>(p + 16, pack_vec<Q8_T_F32>(hi), left - 4);
     } else if (type == Q8_T_F16)
-        store16<Q8_T_F16, false>((uint8_t *)((uint16_t *)row + i), pack_vec<Q8_T_F16>(v), left);
+        store16<Q8_T_F16, true>((uint8_t *)((uint16_t *)row + i), pack_vec<Q8_T_F16>(v), left);
     else
-        store16<Q8_T_BF16, false>((uint8_t *)((uint16_t *)row + i), pack_vec<Q8_T_BF16>(v), left);
+        store16<Q8_T_BF16, true>((uint8_t *)((uint16_t *)row + i), pack_vec<Q8_T_BF16>(v), left);
 }
 
 // fp32 values as the type holds them.
@@ -95,128 +102,243 @@ __device__ __forceinline__ double row_sum(double s, double *part)
     return s;
 }
 
-// ROW threads per row, P pieces of 8 values each.
-template <int ROW, int P>
-__global__ __launch_bounds__(ROW == 1024 ? 1024 : 256) void norm_kernel(const NormArgs a, int64_t row0)
+__device__ __forceinline__ int type_bytes(int type) { return type == Q8_T_F32 ? 4 : type == Q8_T_I8 ? 1 : 2; }
+
+// One over the square root of a mean square and eps.
+__device__ __forceinline__ double inverse_root(double s, double) { return 1.0 / sqrt(s); }
+__device__ __forceinline__ float inverse_root(double s, float) { return __builtin_amdgcn_rsqf((float)s); }
+
+// A piece as loaded, of 16-bit values (HALF) or of any type.
+template <bool HALF>
+struct Piece {
+    float v[kPiece];
+    __device__ __forceinline__ void load(const void *row, int type, int64_t i, int left) { load8(row, type, i, left, v); }
+    __device__ __forceinline__ void get(int, float (&to)[kPiece]) const
+    {
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) to[j] = v[j];
+    }
+};
+template <>
+struct Piece<true> {
+    u32x4 raw;
+    __device__ __forceinline__ void load(const void *row, int, int64_t i, int left)
+    {
+        const uint8_t *p = (const uint8_t *)row + 2 * i;                   // (either 16-bit type)
+        raw = left >= kPiece ? __builtin_nontemporal_load((const u32x4_any *)p) : load16<Q8_T_BF16>(p, left);
+    }
+    __device__ __forceinline__ void get(int type, float (&to)[kPiece]) const
+    {
+        if (type == Q8_T_F16)
+            unpack16<Q8_T_F16>(raw, to);
+        else
+            unpack16<Q8_T_BF16>(raw, to);
+    }
+};
+
+// ROW threads per row, P pieces of 8 values each.  HALF: x, the residual and
+// gates by row are of 16-bit types.
+template <int ROW, int P, bool WIDE, bool HALF>
+__global__ __launch_bounds__(ROW > 256 ? ROW : 256) void norm_kernel(const NormArgs a)
 {
-    __shared__ double part[4][ROW / 64];
-    __shared__ uint32_t part_max[ROW / 64];
-    const int t = threadIdx.x % ROW;
-    const int64_t row = row0 + (ROW == 64 ? (int64_t)blockIdx.x * 4 + threadIdx.x / 64 : blockIdx.x);
-    if (ROW == 64 && row >= a.m) return;
-    const int n = a.n;
-    auto bytes = [](int type) { return type == Q8_T_F32 ? 4 : type == Q8_T_I8 ? 1 : 2; };
-    const uint8_t *x = (const uint8_t *)a.x + row * a.x_stride * bytes(a.x_type);
-
-    float v[P][kPiece];
-#pragma unroll
-    for (int p = 0; p < P; ++p) load8(x, a.x_type, (t + ROW * p) * kPiece, n - (t + ROW * p) * kPiece, v[p]);
-
-    // mean and 1 / sqrt(mean square + eps) of the row held
-    double mean = 0.0, rstd;
-    auto stats = [&](double *p0, double *p1) {
-        if (a.layer) {
-            double s = 0.0;
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-                for (int j = 0; j < kPiece; ++j) s += (double)v[p][j];
-            mean = row_sum<ROW>(s, p0) / n;
-        }
-        double s = 0.0;
+    typedef typename std::conditional<WIDE, double, float>::type R;
+    constexpr bool FEW = P <= (HALF ? 4 : 2);   // a row's loads all at once
+    constexpr bool AHEAD = FEW && HALF;         // and the next row's before its work
+    constexpr int kPer = ROW == 64 ? 4 : 1, K = FEW ? P : 1;
+    __shared__ double part[2][4][ROW / 64];
+    __shared__ uint32_t part_max[2][ROW / 64];
+    const int t = threadIdx.x % ROW, n = a.n;
+    const double inv_n = 1.0 / n;
+    int begin;                             // of this thread's values
+    auto at = [&](int p) { return begin + ROW * p * kPiece; };
+    const bool gate_row = a.gate && a.gate_stride != 0;
+    float w[K][kPiece] = {}, pw[K][kPiece] = {};
+    bool first = true;
+    int odd = 0;                           // LDS of one row and the next
+    Piece<HALF> xs[P], rs[K], gs[K];
+    auto load_row = [&](int64_t row) {
+        const uint8_t *x = (const uint8_t *)a.x + row * a.x_stride * type_bytes(a.x_type);
+        const uint8_t *r = (const uint8_t *)a.residual + row * a.r_stride * type_bytes(a.r_type);
+        const uint8_t *g = (const uint8_t *)a.gate + row * a.gate_stride * type_bytes(a.gate_type);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int left = n - (t + ROW * p) * kPiece;
-#pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                const double d = (double)v[p][j] - mean;
-                if (!a.layer || j < left) s = fma(d, d, s);
-            }
+            const int i = at(p), left = n - i;
+            xs[p].load(x, a.x_type, i, left);
+            if (FEW && a.residual) rs[p].load(r, a.r_type, i, left);
+            if (FEW && gate_row) gs[p].load(g, a.gate_type, i, left);
         }
-        rstd = 1.0 / sqrt(row_sum<ROW>(s, p1) / n + (double)a.eps);
     };
+    for (int64_t row = (int64_t)blockIdx.x * kPer + threadIdx.x / ROW; row < a.m;
+         row += (int64_t)gridDim.x * kPer, odd ^= 1) {
+        // (formed in every turn: addresses and converted weights carried over the
+        // loop would take the registers of several waves)
+        begin = t * kPiece;
+        asm volatile("" : "+v"(begin));
+#pragma unroll
+        for (int p = 0; p < K; ++p)
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) asm volatile("" : "+v"(w[p][j]), "+v"(pw[p][j]));
+        const uint8_t *r = (const uint8_t *)a.residual + row * a.r_stride * type_bytes(a.r_type);
+        const uint8_t *g = (const uint8_t *)a.gate + row * a.gate_stride * type_bytes(a.gate_type);
+        float v[P][kPiece];
+        if (!AHEAD || first) load_row(row);
+        if (FEW && first) {                // (kept where rows are many)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int i = at(p), left = n - i;
+                if (a.post) load8(a.post_weight, Q8_T_F32, i, left, pw[p]);
+                load8(a.weight, Q8_T_F32, i, left, w[p]);
+            }
+            first = false;
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) xs[p].get(a.x_type, v[p]);
+        Piece<HALF> rn[K], gn[K];
+        if (AHEAD) {                       // the next row's streams are on their way during this one's work
+#pragma unroll
+            for (int p = 0; p < K; ++p) {
+                rn[p] = rs[p];
+                gn[p] = gs[p];
+            }
+            const int64_t next = row + (int64_t)gridDim.x * kPer;
+            if (next < a.m) load_row(next);
+        }
+        // the row held as (v - pivot) - middle, and 1 / sqrt(mean square + eps)
+        R pivot = 0, middle = 0, rstd;
+        auto centred = [&](float x) { return a.layer ? ((R)x - pivot) - middle : (R)x; };
+        auto stats = [&](double *p0, double *p1) {
+            if (a.layer) {
+                pivot = WIDE ? (R)0 : (R)v[0][0];
+                middle = 0;
+                R s = 0;
+                int mine = 0;
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const int left = n - at(p);
+                    mine += max(0, min(kPiece, left));
+#pragma unroll
+                    for (int j = 0; j < kPiece; ++j) s += j < left ? (R)v[p][j] - pivot : (R)0;
+                }
+                const double mean = row_sum<ROW>((double)s + (double)pivot * mine, p0) * inv_n;
+                middle = (R)(mean - (double)pivot);
+            }
+            R s = 0;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int left = n - at(p);
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) {
+                    const R d = j < left ? centred(v[p][j]) : (R)0;
+                    s = fma(d, d, s);
+                }
+            }
+            rstd = inverse_root(row_sum<ROW>((double)s, p1) * inv_n + (double)a.eps, (R)0);
+        };
 
-    if (a.residual) {
-        if (a.post) stats(part[0], part[1]);
-        const uint8_t *r = (const uint8_t *)a.residual + row * a.r_stride * bytes(a.r_type);
-        const uint8_t *g = (const uint8_t *)a.gate + row * a.gate_stride * bytes(a.gate_type);
-        uint8_t *ro = (uint8_t *)a.residual_out + row * a.ro_stride * bytes(a.r_type);
+        if (a.residual) {
+            if (a.post) stats(part[odd][0], part[odd][1]);
+            uint8_t *ro = (uint8_t *)a.residual_out + row * a.ro_stride * type_bytes(a.r_type);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int i = at(p), left = n - i, k = FEW ? p : 0;
+                if (left <= 0) continue;
+                float rv[kPiece], gv[kPiece], pb[kPiece];
+                if (!FEW) {
+                    __builtin_amdgcn_sched_barrier(0);     // (one piece at a time: registers)
+                    rs[0].load(r, a.r_type, i, left);
+                    if (gate_row) gs[0].load(g, a.gate_type, i, left);
+                    if (a.post) load8(a.post_weight, Q8_T_F32, i, left, pw[0]);
+                }
+                (AHEAD ? rn : rs)[k].get(a.r_type, rv);
+                if (gate_row) (AHEAD ? gn : gs)[k].get(a.gate_type, gv);
+                else if (a.gate) load8(a.gate, a.gate_type, i, left, gv);
+                if (a.post_bias) load8(a.post_bias, Q8_T_F32, i, left, pb);
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) {
+                    R y = (R)v[p][j];
+                    if (a.post) {
+                        y = centred(v[p][j]) * rstd * (R)pw[k][j];
+                        if (a.post_bias) y += (R)pb[j];
+                    }
+                    if (a.gate) y *= (R)gv[j];
+                    v[p][j] = as_stored((float)fma((R)a.residual_scale, (R)rv[j], y), a.r_type);
+                    if (j >= left) v[p][j] = 0.0f;
+                }
+                store8(ro, a.r_type, i, left, v[p]);
+            }
+        }
+
+        stats(part[odd][2], part[odd][3]);
+        const bool codes = a.y_type == Q8_T_I8;
+        uint8_t *y = (uint8_t *)a.y + row * a.y_stride * type_bytes(a.y_type);
+        uint32_t amax = 0;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int i = (t + ROW * p) * kPiece, left = n - i;
+            const int i = at(p), left = n - i, k = FEW ? p : 0;
             if (left <= 0) continue;
-            float rv[kPiece], gv[kPiece], wv[kPiece], bv[kPiece];
-            load8(r, a.r_type, i, left, rv);
-            if (a.gate) load8(g, a.gate_type, i, left, gv);
-            if (a.post) load8(a.post_weight, Q8_T_F32, i, left, wv);
-            if (a.post_bias) load8(a.post_bias, Q8_T_F32, i, left, bv);
+            float b[kPiece];
+            if (!FEW) {
+                __builtin_amdgcn_sched_barrier(0);
+                load8(a.weight, Q8_T_F32, i, left, w[0]);
+            }
+            if (a.bias) load8(a.bias, Q8_T_F32, i, left, b);
 #pragma unroll
             for (int j = 0; j < kPiece; ++j) {
-                double y = v[p][j];
-                if (a.post) {
-                    y = (y - mean) * rstd * (double)wv[j];
-                    if (a.post_bias) y += (double)bv[j];
-                }
-                if (a.gate) y *= (double)gv[j];
-                v[p][j] = as_stored((float)fma((double)a.residual_scale, (double)rv[j], y), a.r_type);
-                if (j >= left) v[p][j] = 0.0f;
+                R o = centred(v[p][j]) * rstd * (R)w[k][j];
+                if (a.bias) o += (R)b[j];
+                v[p][j] = (float)o;
+                if (j < left) amax = max(amax, abs_bits(v[p][j]));
             }
-            store8(ro, a.r_type, i, left, v[p]);
+            if (!WIDE || !codes) store8(y, a.y_type, i, left, v[p]);
         }
-    }
-
-    stats(part[2], part[3]);
-    const bool codes = a.y_type == Q8_T_I8;
-    uint8_t *y = (uint8_t *)a.y + row * a.y_stride * bytes(a.y_type);
-    uint32_t amax = 0;
+        if (!WIDE || !codes) continue;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int i = (t + ROW * p) * kPiece, left = n - i;
-        if (left <= 0) continue;
-        float wv[kPiece], bv[kPiece];
-        load8(a.weight, Q8_T_F32, i, left, wv);
-        if (a.bias) load8(a.bias, Q8_T_F32, i, left, bv);
+        for (int d = 32; d; d >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d));
+        if constexpr (ROW > 64) {
+            if ((threadIdx.x & 63) == 0) part_max[odd][threadIdx.x >> 6] = amax;
+            __syncthreads();
+            amax = 0;
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) {
-            double o = ((double)v[p][j] - mean) * rstd * (double)wv[j];
-            if (a.bias) o += (double)bv[j];
-            v[p][j] = (float)o;
-            if (j < left) amax = max(amax, abs_bits(v[p][j]));
+            for (int k = 0; k < ROW / 64; ++k) amax = max(amax, part_max[odd][k]);
         }
-        if (!codes) store8(y, a.y_type, i, left, v[p]);
-    }
-    if (!codes) return;
+        const float s = row_scale(amax);
+        if (t == 0) a.y_scale[row] = s;
+        const RowCoder rc(s);
 #pragma unroll
-    for (int d = 32; d; d >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d));
-    if constexpr (ROW > 64) {
-        if ((threadIdx.x & 63) == 0) part_max[threadIdx.x >> 6] = amax;
-        __syncthreads();
-        amax = 0;
-#pragma unroll
-        for (int w = 0; w < ROW / 64; ++w) amax = max(amax, part_max[w]);
-    }
-    const float s = row_scale(amax);
-    if (t == 0) a.y_scale[row] = s;
-    const RowCoder rc(s);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int i = (t + ROW * p) * kPiece;       // (n is a multiple of 32)
-        if (i < n) *(u32x2 *)(y + i) = (u32x2){rc.code4(v[p]), rc.code4(v[p] + 4)};
+        for (int p = 0; p < P; ++p) {
+            const int i = at(p);            // (n is a multiple of 32)
+            if (i < n) *(u32x2 *)(y + i) = (u32x2){rc.code4(v[p]), rc.code4(v[p] + 4)};
+        }
     }
 }
 
-template <int ROW, int P>
+// Workgroups: one per row (four rows, by waves), or as many as the device holds,
+// which then take several (16384 x 4096 bfloat16: 133 us, with twice or two
+// thirds as many 144 and 169).
+template <int ROW, int P, bool WIDE, bool HALF>
 int launch(const NormArgs &a, hipStream_t stream)
 {
-    constexpr int64_t per = ROW == 64 ? 4 : 1, most = per << (ROW == 1024 ? 21 : 23);
-    // (2^32 threads bound a launch)
-    for (int64_t r = 0; r < a.m; r += most) {
-        const int64_t rows = a.m - r < most ? a.m - r : most;
-        hipLaunchKernelGGL((norm_kernel<ROW, P>), dim3((unsigned)((rows + per - 1) / per)),
-                           dim3(ROW == 1024 ? 1024 : 256), 0, stream, a, r);
-        if (hipGetLastError() != hipSuccess) return -6;
-    }
-    return 0;
+    constexpr int64_t per = ROW == 64 ? 4 : 1, threads = ROW > 256 ? ROW : 256;
+    static const int resident = [] {
+        int n = 0;
+        const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_kernel<ROW, P, WIDE, HALF>,
+                                                                          (int)threads, 0);
+        return 256 * (e == hipSuccess && n > 0 ? n : 1);       // (256 CUs)
+    }();
+    const int64_t groups = (a.m + per - 1) / per;
+    hipLaunchKernelGGL((norm_kernel<ROW, P, WIDE, HALF>), dim3((unsigned)(groups < resident ? groups : resident)),
+                       dim3((unsigned)threads), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? 0 : -6;
+}
+
+template <int ROW, int P>
+int launch_shape(const NormArgs &a, hipStream_t stream)
+{
+    auto half = [](int type) { return type == Q8_T_F16 || type == Q8_T_BF16; };
+    const bool halves = half(a.x_type) && (!a.residual || half(a.r_type)) &&
+                        (!a.gate || a.gate_stride == 0 || half(a.gate_type));
+    if (!halves) return launch<ROW, P, true, false>(a, stream);
+    return half(a.y_type) ? launch<ROW, P, false, true>(a, stream) : launch<ROW, P, true, true>(a, stream);
 }
 
 }  // namespace
@@ -224,14 +346,14 @@ int launch(const NormArgs &a, hipStream_t stream)
 int launch_norm(const NormArgs &a, hipStream_t stream)
 {
     const int n = a.n;
-    if (n <= 512) return launch<64, 1>(a, stream);
-    if (n <= 1024) return launch<64, 2>(a, stream);
-    if (n <= 2048) return launch<256, 1>(a, stream);
-    if (n <= 4096) return launch<256, 2>(a, stream);
-    if (n <= 8192) return launch<256, 4>(a, stream);
-    if (n <= 16384) return launch<256, 8>(a, stream);
-    if (n <= 32768) return launch<1024, 4>(a, stream);
-    return launch<1024, 8>(a, stream);
+    if (n <= 512) return launch_shape<64, 1>(a, stream);
+    if (n <= 1024) return launch_shape<64, 2>(a, stream);
+    if (n <= 2048) return launch_shape<256, 1>(a, stream);
+    if (n <= 4096) return launch_shape<256, 2>(a, stream);
+    if (n <= 8192) return launch_shape<512, 2>(a, stream);
+    if (n <= 16384) return launch_shape<512, 4>(a, stream);
+    if (n <= 32768) return launch_shape<512, 8>(a, stream);
+    return launch_shape<512, 16>(a, stream);
 }
 
 }  // namespace q8

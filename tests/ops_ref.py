@@ -56,28 +56,40 @@ def product_act(cx, sx, cw, sw, bias, act, residual):
 # Norms.  The 64-bit arithmetic of either side is off by a few n 2^-53 of the
 # sums' terms, below 2^-36 for n <= 65536; a mean taken off a row far from 0
 # multiplies that by the terms' size.
+#
+# Rows that are all of 16-bit types are computed in 32 bits (`narrow`), by
+# differences from a value p of the row, c = (x - p) - (mean - p): two differences
+# and one rounding of mean - p, of terms below |c| + cmax and cmax, are off by
+# u (2 |c| + 3 cmax).  The squares' sums of up to 128 terms a thread carry 130 u,
+# their inverse root 65 u and 2 u of the instruction; three products and sums
+# 3 u of the value before the bias and u of the value.
 
 REL64 = 2.0 ** -36
 
 
-def norm(x, weight, bias, eps, layer):
-    """(value, bound of the 64-bit arithmetic) of rows x (fp64)."""
+def norm(x, weight, bias, eps, layer, narrow=False):
+    """(value, bound of the arithmetic) of rows x (fp64)."""
     mean = x.mean(axis=1, keepdims=True) if layer else 0.0
     d = x - mean
     r = 1 / np.sqrt((d * d).mean(axis=1, keepdims=True) + float(np.float32(eps)))
     y = d * r * weight
     size = (np.abs(x) + np.abs(mean)) * r * np.abs(weight)
+    bound = REL64 * size
+    if narrow:
+        far = np.abs(d).max(axis=1, keepdims=True) if layer else 0.0
+        bound = bound + 1.01 * U * (r * np.abs(weight) * (2 * np.abs(d) + 3 * far) + 71 * np.abs(y))
     if bias is not None:
         y = y + bias
-        size = size + np.abs(bias)
-    return y, REL64 * size
+        bound = bound + REL64 * np.abs(bias) + (U * np.abs(y) if narrow else 0)
+    return y, bound
 
 
-def residual(x, r, post_weight, post_bias, gate, residual_scale, eps, layer):
-    a, b = norm(x, post_weight, post_bias, eps, layer) if post_weight is not None else (x, 0.0)
+def residual(x, r, post_weight, post_bias, gate, residual_scale, eps, layer, narrow=False):
+    a, b = norm(x, post_weight, post_bias, eps, layer, narrow) if post_weight is not None else (x, 0.0)
     g = 1.0 if gate is None else gate
     y = g * a + float(np.float32(residual_scale)) * r
-    return y, np.abs(g) * b + REL64 * (np.abs(g * a) + np.abs(residual_scale * r))
+    rel = (3 * U if narrow else 0) + REL64            # the gate's product and the fused sum
+    return y, np.abs(g) * b + rel * (np.abs(g * a) + np.abs(residual_scale * r))
 
 
 def assert_rounded(got, value, bound, t, what):

@@ -37,15 +37,23 @@ def _vec(rng, n, size=0.2, middle=1.0):
     return to_gpu((rng.normal(size=n) * size + middle).astype(np.float32))
 
 
-def _check_y(q, x, weight, bias, eps, layer, out, t, what):
+def _narrow(yt, *streams):
+    """Whether a call with these rows is computed in 32 bits."""
+    import torch
+    half = (torch.float16, torch.bfloat16)
+    return yt in ("fp16", "bf16") and all(s is None or s.dtype in half for s in streams)
+
+
+def _check_y(q, x, weight, bias, eps, layer, out, t, what, narrow=None):
     """y of the rows x (as the norm read them)."""
+    narrow = _narrow(t, x) if narrow is None else narrow
     if t == "i8":
         y, _ = ops_ref.norm(_host(x), _host(weight), _host(bias), eps, layer)
         codes, scale = i8_ref.quantize(y.astype(np.float32))
         assert np.array_equal(out.y.cpu().numpy(), codes), what
         assert np.array_equal(out.y_scale.cpu().numpy(), scale, equal_nan=True), what
     else:
-        value, bound = ops_ref.norm(_host(x), _host(weight), _host(bias), eps, layer)
+        value, bound = ops_ref.norm(_host(x), _host(weight), _host(bias), eps, layer, narrow)
         ops_ref.assert_rounded(_host(out.y), value, bound, t, what)
 
 
@@ -104,12 +112,14 @@ def test_residual(q, m, n, types, case):
     yd = torch.int8 if yt == "i8" else i8_ref.torch_type(yt)
     out = q.residual_norm_rows(x, r, w, bias=b, post_weight=pw, post_bias=pb, gate=gate, residual_scale=alpha,
                                eps=1e-6, layer=layer, dtype=yd)
-    value, bound = ops_ref.residual(_host(x), _host(r), _host(pw), _host(pb), _host(gate), alpha, 1e-6, layer)
+    narrow = _narrow(yt, x, r, gate if case.get("gate") == "row" else None)
+    value, bound = ops_ref.residual(_host(x), _host(r), _host(pw), _host(pb), _host(gate), alpha, 1e-6, layer, narrow)
     ops_ref.assert_rounded(_host(out.residual), value, bound, rt, "residual")
-    _check_y(q, out.residual, w, b, 1e-6, layer, out, yt, "y")
+    _check_y(q, out.residual, w, b, 1e-6, layer, out, yt, "y", narrow)
     # what follows the stream's update is the plain norm of the stream
-    plain = q.norm_rows(out.residual, w, bias=b, eps=1e-6, layer=layer, dtype=yd)
-    assert torch.equal(plain.y, out.y)
+    if narrow == _narrow(yt, r):
+        plain = q.norm_rows(out.residual, w, bias=b, eps=1e-6, layer=layer, dtype=yd)
+        assert torch.equal(plain.y, out.y)
     # in place
     again = q.residual_norm_rows(x, r, w, bias=b, post_weight=pw, post_bias=pb, gate=gate, residual_scale=alpha,
                                  eps=1e-6, layer=layer, residual_out=r, dtype=yd)
@@ -130,13 +140,23 @@ def test_row_starts(q, offset, pad, t):
         bufs = [torch.full((m * (n + pad) + offset + 8,), -7.0, dtype=tt, device="cuda") for _ in range(2)]
         ro, y = (b[offset:offset + m * (n + pad)].view(m, n + pad)[:, :n] for b in bufs)
         out = q.residual_norm_rows(x, r, w, gate=g, residual_out=ro, y=y)
-        value, bound = ops_ref.residual(_host(x), _host(r), None, None, _host(g), 1.0, 1e-5, False)
+        value, bound = ops_ref.residual(_host(x), _host(r), None, None, _host(g), 1.0, 1e-5, False, _narrow(t, x))
         ops_ref.assert_rounded(_host(ro), value, bound, t, "residual")
         _check_y(q, ro, w, None, 1e-5, False, out, t, "y")
         for b in bufs:
             body = b[offset:offset + m * (n + pad)].view(m, n + pad)
             assert bool((body[:, n:] == -7).all()) and bool((b[:offset] == -7).all())
             assert bool((b[offset + m * (n + pad):] == -7).all())
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+def test_rows_far_from_zero(q, t):
+    """A mean far above the spread, 16-bit rows."""
+    rng = synth.rng("normfar", t)
+    x = _tensor(rng, 5, 900, t, middle=300.0)
+    w, b = _vec(rng, 900), _vec(rng, 900, 0.1, 0.0)
+    out = q.norm_rows(x, w, bias=b, layer=True, dtype=i8_ref.torch_type(t))
+    _check_y(q, x, w, b, 1e-5, True, out, t, "y")
 
 
 def test_odd_rows(q):
@@ -186,5 +206,5 @@ def test_many_rows(q):
     w = torch.ones(n, device="cuda")
     out = q.norm_rows(x, w, eps=0.0, dtype=torch.bfloat16)
     assert bool((out.y[:m // 2] == 1).all()) and bool((out.y[-1] == 1).all())
-    value, bound = ops_ref.norm(_host(x[m // 2:m // 2 + 1]), np.ones(n), None, 0.0, False)
+    value, bound = ops_ref.norm(_host(x[m // 2:m // 2 + 1]), np.ones(n), None, 0.0, False, True)
     ops_ref.assert_rounded(_host(out.y[m // 2:m // 2 + 1]), value, bound, "bf16", "row")

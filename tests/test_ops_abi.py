@@ -109,6 +109,15 @@ def test_sample_workspace_bytes():
         assert lib.sample_workspace_bytes(m, v) == 0
 
 
+def test_a_workspace_serves_smaller_calls():
+    """Room made for m rows of n logits is enough for fewer of either, of any
+    type."""
+    need = lambda m, v: q.sample_workspace_bytes(m, v)
+    for m in (1, 2, 7, 64, 511, 512, 513, 2048, 2049, 5000):
+        for v in (10, 4096, 4097, 32000, 65536, 262144, 1 << 24):
+            assert all(need(a, b) <= need(m, v) for a in {1, m // 2, max(1, m - 1)} - {0} for b in {1, v // 2, v - 1, v})
+
+
 # --- the binding -------------------------------------------------------------
 
 def _bad(fn, ok, exc, match, **kw):
