@@ -57,8 +57,9 @@ constexpr int kOut = 0x7ff00000;  // an offset past every resource: reads zero
 // One tile: outputs n0 .. (TN of them, TN/2 gated), tokens m0 .. m0 + TM - 1.
 // w0 .. x1: the stages, separate LDS objects, so that a fragment read waits for
 // its own stage's loads only.  STREAM: outputs are written past the caches.  EPI:
-// y = act(value) + residual.
-template <int TN, int TM, int WN, int WM, int YT, bool GATED, bool STREAM, bool EPI>
+// y = act(value) + residual.  KS 2: two groups of WN x WM waves take half of k each,
+// in stages of their own (the second behind the first's), and join their sums.
+template <int TN, int TM, int WN, int WM, int YT, bool GATED, bool STREAM, bool EPI, int KS = 1>
 __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0, uint8_t *w0,
                                         uint8_t *w1, uint8_t *w2, uint8_t *x0, uint8_t *x1)
 {
@@ -71,17 +72,23 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
     static_assert(kWaves % 2 == 0, "the chunk of a lane is the same for every load");
     static_assert(!GATED || NI % 2 == 0, "gate and up halves");
 
-    const int wave = wave_uniform((int)(threadIdx.x >> 6));
+    const int wave_all = wave_uniform((int)(threadIdx.x >> 6));
+    const int part = KS == 1 ? 0 : wave_all / kWaves, wave = KS == 1 ? wave_all : wave_all % kWaves;
     const int lane = threadIdx.x & 63;
     const int wn = wave / WM, wm = wave % WM;
     const int h = lane >> 5, li = lane & 31;
 
-    // operand rows of the tile
-    const int k = (int)a.k;
+    // operand rows of the tile; bytes k_begin .. k_begin + k - 1 of them
+    const int k_first = KS == 1 ? (int)a.k : ((int)a.k / 2 + kStep - 1) / kStep * kStep;
+    const int k_begin = part ? k_first : 0, k = part ? (int)a.k - k_first : k_first;
+    if constexpr (KS > 1) {
+        w0 += part * TN * kStep; w1 += part * TN * kStep; w2 += part * TN * kStep;
+        x0 += part * TM * kStep; x1 += part * TM * kStep;
+    }
     const int w_rows = (int)min((int64_t)kCols, a.n - n0), x_rows = (int)min((int64_t)TM, a.m - m0);
     const int w_stride = (int)a.w_stride, x_stride = (int)a.x_stride;
     const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(a.x + m0 * a.x_stride), 0, (x_rows - 1) * x_stride + k, kBufferWord3);
+        (void *)(a.x + m0 * a.x_stride + k_begin), 0, (x_rows - 1) * x_stride + k, kBufferWord3);
     const int8_t *w_base[kLoadsW];     // (no array of resources: the host pass has no such type)
     int voff[kLoadsW + kLoadsX];
     // load u of a wave: staged rows 8f .. 8f+7, f = wave + kWaves * u
@@ -91,7 +98,7 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
     for (int u = 0; u < kLoadsW; ++u) {
         const int b = 8 * (wave + kWaves * u);          // of TN; 32-row groups are uniform
         int row = b;
-        const int8_t *base = a.w + n0 * a.w_stride;
+        const int8_t *base = a.w + n0 * a.w_stride + k_begin;
         if (GATED) {
             const int grp = b / 32 % NI, half = grp / (NI / 2);
             row = b / (32 * NI) * kWaveCols + 32 * (grp % (NI / 2)) + b % 32;
@@ -131,7 +138,7 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
 
     // what the outputs need: one weight row's scale and bias per thread, the
     // scales of the lane's tokens
-    const int tid = threadIdx.x;
+    const int tid = KS == 1 ? (int)threadIdx.x : (int)threadIdx.x % (64 * kWaves);
     float w_scale = 0.0f, w_bias = 0.0f, s_x[MI];
     static_assert(TN <= 64 * kWaves, "a thread per weight row");
     if (tid < TN) {
@@ -198,7 +205,7 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
         asm volatile("" ::: "memory");
     };
 
-    const int steps = (k + kStep - 1) / kStep;
+    const int steps = (k_first + kStep - 1) / kStep;     // (as many for either part: the barriers are shared)
     Frag f0, f1;
     issue_w(0, w0);
     issue_x(0, x0);
@@ -242,6 +249,35 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
     if (st + 3 < steps) body(st + 3, w0, w1, x1, x0);
     if (st + 4 < steps) body(st + 4, w1, w2, x0, x1);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (zeros still on their way to LDS)
+    if constexpr (KS > 1) {
+        static_assert(KS == 2 && kWaves == 2 && NI * MI * 4 * 1024 <= TN * kStep, "a stage of the second part per wave");
+        __syncthreads();
+        const int over = part ? 0 : TN * kStep;        // the second part's stages
+        v4i *sums = (v4i *)((wave ? w1 : w0) + over);
+        if (part)
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < MI; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        sums[((i * MI + j) * 4 + q) * 64 + lane] = (v4i){acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                                        acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        __syncthreads();
+        if (!part)
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < MI; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const v4i s = sums[((i * MI + j) * 4 + q) * 64 + lane];
+                        acc[i][j][4 * q] += s.x;
+                        acc[i][j][4 * q + 1] += s.y;
+                        acc[i][j][4 * q + 2] += s.z;
+                        acc[i][j][4 * q + 3] += s.w;
+                    }
+    }
 
     // Outputs.  Result r of a lane: weight row 8(r/4) + 4h + r%4 of its tile,
     // token li.  The tile's scales (and bias) go to LDS, and every wave turns its
@@ -254,6 +290,7 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
         if (!GATED) scales[TN + tid] = w_bias;
     }
     __syncthreads();
+    if (KS > 1 && part) return;
     constexpr int kES = YT == Q8_T_F32 ? 4 : 2;
     constexpr int kOutTiles = GATED ? NI / 2 : NI;
     constexpr int kPass = kOutTiles < 4 / kES ? kOutTiles : 4 / kES;    // tiles side by side
@@ -447,6 +484,22 @@ __global__ __launch_bounds__(256, 2) void i8_medium_kernel(const I8Args a, const
                                                w0, w1, w2, x0, x1);
 }
 
+// 128 x 64 by two pairs of waves, each over half of k, with an epilogue only: for
+// products with few outputs and a long k, whose tiles of 128 x 128 would leave half
+// of the CUs without one and are bound by the round trip of each of their steps.
+template <int YT, bool STREAM>
+__global__ __launch_bounds__(256) void i8_narrow_kernel(const I8Args a, const TileGrid g)
+{
+    __shared__ __align__(16) uint8_t w0[2 * 128 * kStep];
+    __shared__ __align__(16) uint8_t w1[2 * 128 * kStep];
+    __shared__ __align__(16) uint8_t w2[2 * 128 * kStep];
+    __shared__ __align__(16) uint8_t x0[2 * 64 * kStep];
+    __shared__ __align__(16) uint8_t x1[2 * 64 * kStep];
+    int tn, tm;
+    g.at(xcd_run(blockIdx.x, g.tiles_n * g.tiles_m), tn, tm);
+    i8_tile<128, 64, 2, 1, YT, false, STREAM, true, 2>(a, (int64_t)tn * 128, (int64_t)tm * 64, w0, w1, w2, x0, x1);
+}
+
 TileGrid tile_grid(const I8Args &a, bool gated, int tile)
 {
     const int64_t cols = gated ? tile / 2 : tile;
@@ -488,6 +541,15 @@ int launch_form(const I8Args &a, hipStream_t stream)
     const Plan p = plan(a, GATED);
     const int tiles = p.grid.tiles_n * p.grid.tiles_m;
     if (!tiles) return Q8_E_UNSUPPORTED;
+    if constexpr (EPI)
+        // (512 x 14336 x 4096 59 -> 45 us, 512 x 4096 x 4096 23 -> 20, 700 x 2048 x 2000
+        // 19.4 -> 16.8; a short k gains nothing: 300 x 256 x 4096 9.7 -> 10.7)
+        if (!p.large && tiles <= 128 && a.k >= 1024) {
+            const TileGrid g = {p.grid.tiles_n, (int)((a.m + 63) / 64), 0};
+            hipLaunchKernelGGL((i8_narrow_kernel<YT, STREAM>), dim3((unsigned)(g.tiles_n * g.tiles_m)), dim3(256), 0,
+                               stream, a, g);
+            return hipGetLastError() == hipSuccess ? 0 : -6;
+        }
     if (p.large)
         hipLaunchKernelGGL((i8_large_kernel<YT, GATED, STREAM, EPI>), dim3((unsigned)(2 * tiles - p.grid.whole)),
                            dim3(512), 0, stream, a, p.grid);

@@ -62,6 +62,21 @@ def test_sizes(q, m, k, n, t):
         _check(q, c, t, act, bias=i % 2 == 0, residual=i % 3 != 1)
 
 
+@pytest.mark.parametrize("t", i8_ref.TYPES)
+@pytest.mark.parametrize("m,k,n", [(300, 1024, 4100), (300, 1056, 4100), (130, 2080, 6000), (97, 1312, 8192),
+                                   (512, 4128, 3001), (320, 14336, 4096)])
+def test_halves_of_k(q, m, k, n, t):
+    """Few outputs and a long k: halves of k side by side, of one and of
+    different lengths, the second ending inside a step; bits as i8_matmul."""
+    import torch
+    c = Case(m, k, n, "halves")
+    for act, bias, residual in (("none", True, True), ("silu", False, False)):
+        _check(q, c, t, act, bias=bias, residual=residual)
+    cx, sx, cw, sw, b, r = c.gpu(t)
+    plain = q.i8_matmul(cx, cw, sw, x_scale=sx, bias=b, dtype=i8_ref.torch_type(t))
+    assert torch.equal(q.i8_matmul_act(cx, cw, sw, x_scale=sx, bias=b, dtype=i8_ref.torch_type(t)), plain)
+
+
 def test_forms(q):
     """The sizes above reach every kernel."""
     forms = {q.raw.q8v_i8_form(n, k, m, 0) for m, k, n in SIZES}
