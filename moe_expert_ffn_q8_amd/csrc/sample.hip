@@ -12,9 +12,9 @@
 // exact, whatever their order, and a border of top-p or of the random number
 // falls between tokens as it does in 64 bits.
 //
-// The logits are read once.  A workgroup takes a row, or a part of one, sums its
-// weights where a filter needs the sum, and lists the logits that reach a bound:
-// that many of its lanes' maxima do.  The list is a head of the row's order (down
+// The logits are read once.  A workgroup takes a short row, a wave a part of a long
+// one, sums its weights where a filter needs the sum, and lists the logits that
+// reach a bound: as many lanes' maxima do as are wanted.  The list is a head of the row's order (down
 // to the largest bound of its parts), and where the answers lie in it, as they do
 // for most rows, it alone is looked at further.  The other rows (a head that goes
 // beyond the list, many equal logits) are read again: for a histogram of all
@@ -24,6 +24,12 @@
 // A sum in 64 bits costs 20 vector instructions a logit, one in 32 bits 7.  For
 // top-p the latter is enough where the answer is the same over the range of its
 // error; the few rows where it is not are read again.
+//
+// Bounds: vector instructions for many long rows (512 x 262144 bfloat16, top-p:
+// parts 72 us, of which the pipe is busy 82%, join 13; HBM's floor 38); else the
+// chain of launches, round trips and barriers: 1 x 32000 5.8 + 11.6 us, 8 x 262144
+// 6.4 + 13, 333 x 50257 with settings of their own 20 + 13, and 7 + 28 where a row
+// is read again.
 #include "i8_device.h"
 #include "order_device.h"
 #include "q8_ops.h"
@@ -989,8 +995,10 @@ struct Work {
     int n_parts, part_len, rank;
 };
 
-// A part is a wave's: what is done once a part (statistics, bound, list) is 350
-// instructions a wave, without barriers, against 17 a logit.
+// A part is a wave's, without barriers.  What is done once a part (statistics,
+// bound, list) is 400 instructions, against 10 a logit; twice the vectors would
+// halve that share but leave nine waves to a CU (512 x 262144: 90 us against 72;
+// parts by four waves of as many vectors 89 to 150).
 constexpr int kPartThreads = 64, kPartVecs = 8;
 
 template <int T>
