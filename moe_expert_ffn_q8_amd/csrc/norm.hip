@@ -109,7 +109,11 @@ __device__ __forceinline__ int type_bytes(int type) { return type == Q8_T_F32 ? 
 
 // One over the square root of a mean square and eps.
 __device__ __forceinline__ double inverse_root(double s, double) { return 1.0 / sqrt(s); }
-__device__ __forceinline__ float inverse_root(double s, float) { return __builtin_amdgcn_rsqf((float)s); }
+__device__ __forceinline__ float inverse_root(double s, float)
+{
+    if (!(s > 1e-30 && s < 1e37)) return (float)(1.0 / sqrt(s));
+    return __builtin_amdgcn_rsqf((float)s);
+}
 
 // A piece as loaded, of 16-bit values (HALF) or of any type.
 template <bool HALF>
@@ -235,7 +239,20 @@ __global__ __launch_bounds__(ROW > 256 ? ROW : 256) void norm_kernel(const NormA
                     s = fma(d, d, s);
                 }
             }
-            rstd = inverse_root(row_sum<ROW>((double)s, p1) * inv_n + (double)a.eps, (R)0);
+            double sum = (double)s;
+            if (!WIDE && !(s > 1e-30f && s < 3e38f)) {     // squares that 32 bits do not hold
+                sum = 0.0;
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const int left = n - at(p);
+#pragma unroll
+                    for (int j = 0; j < kPiece; ++j) {
+                        const double d = j < left ? (double)centred(v[p][j]) : 0.0;
+                        sum = fma(d, d, sum);
+                    }
+                }
+            }
+            rstd = inverse_root(row_sum<ROW>(sum, p1) * inv_n + (double)a.eps, (R)0);
         };
 
         if (a.residual) {

@@ -159,6 +159,19 @@ def test_rows_far_from_zero(q, t):
     _check_y(q, x, w, b, 1e-5, True, out, t, "y")
 
 
+@pytest.mark.parametrize("size", [1e-25, 1e-12, 1e19, 1e30])
+@pytest.mark.parametrize("layer", [False, True])
+def test_rows_whose_squares_leave_32_bits(q, size, layer):
+    """bfloat16 rows of very large and very small values, without an eps."""
+    import torch
+    rng = synth.rng("normsquares", str(size), str(layer))
+    for n in (100, 4096):
+        x = to_gpu((rng.normal(size=(3, n)) * size).astype(np.float32)).bfloat16()
+        w = _vec(rng, n)
+        out = q.norm_rows(x, w, eps=0.0, layer=layer, dtype=torch.bfloat16)
+        _check_y(q, x, w, None, 0.0, layer, out, "bf16", (size, n))
+
+
 def test_odd_rows(q):
     """Zero rows, constant rows, rows far from 0, infinities and NaN."""
     import torch
