@@ -74,6 +74,16 @@ constexpr uint32_t kNoBound = 0xffffffffu;        // of a part that has no list
 
 __device__ __forceinline__ float value_of(uint32_t key) { return key_value((uint64_t)key << 32); }
 
+// Half of how far x lies below `top` (finite values: the whole distance may pass
+// fp32's range, as between masks of either sign), in one rounding.
+__device__ __forceinline__ float half_below(float top, float x) { return fmaf(-0.5f, x, 0.5f * top); }
+
+// The bin of x in a histogram by value.
+__device__ __forceinline__ int value_bin(float top, float x, float bin_scale, int bins)
+{
+    return (int)fminf(half_below(top, x) * (2.0f * bin_scale), (float)(bins - 1));
+}
+
 // A row's settings, as they are applied.
 struct Settings {
     float u;
@@ -334,8 +344,8 @@ struct Listed {
     // high, low: no listed value is outside; before: the head before the list
     __device__ void sort(Shared<NT> &s, const Weights &w, float high, float low, Head before)
     {
-        const float reach = fminf(high - low, (float)(kReach / w.scale));
-        const float bin_scale = fminf((float)(NT - 1) / reach, 1e30f);
+        const float reach = fminf(half_below(high, low), (float)(0.5 * kReach / w.scale));
+        const float bin_scale = fminf((float)(NT - 1) / reach, 1e30f);      // of half distances
         __syncthreads();
         s.count[threadIdx.x] = 0;
         s.mass[threadIdx.x] = 0;
@@ -347,7 +357,7 @@ struct Listed {
             if (key[i]) {
                 const float x = key_value(key[i]);
                 mass[i] = w.units(x);
-                bin[i] = (int)fminf((high - x) * bin_scale, (float)(NT - 1));
+                bin[i] = (int)fminf(half_below(high, x) * bin_scale, (float)(NT - 1));
                 atomicAdd(&s.count[bin[i]], 1u);
                 atomicAdd(&s.mass[bin[i]], mass[i]);
             }
@@ -545,14 +555,15 @@ __device__ __forceinline__ Head locate(const SampleArgs &a, int64_t row, const W
     const int first = s.bin;
     uint32_t count = s.first_count[first];
     Head before = s.before;
-    // keys that the bin may hold, a bin's width to spare on either side
+    // keys that the bin may hold, a bin's width to spare on either side (a logit of the
+    // bin lies between the bounds, so that lo <= hi, and every turn below shortens them)
     auto bound = [&](double d) { return value_key((float)((double)w.top - d / (double)bin_scale)); };
     uint32_t hi = first <= 0 ? value_key(w.top) : min(value_key(w.top), bound(first - 1.0));
     uint32_t lo = first == kBins - 1 || bin_scale == 0.0f ? kLeastKey : max(kLeastKey, bound(first + 2.0));
     auto inside = [&](float x, uint32_t k) {
-        return k >= lo && k <= hi && (int)fminf((w.top - x) * bin_scale, (float)(kBins - 1)) == first;
+        return k >= lo && k <= hi && value_bin(w.top, x, bin_scale, kBins) == first;
     };
-    while (lo != hi) {
+    while (lo < hi) {
         __syncthreads();
         if (count <= Shared<NT>::kList) {      // its logits as a list
             if (threadIdx.x == 0) s.listed = 0;
@@ -572,7 +583,7 @@ __device__ __forceinline__ Head locate(const SampleArgs &a, int64_t row, const W
                 each<T, NT>(a, row, take);
             __syncthreads();
             Listed<NT> l;
-            l.take(s, (int)count);
+            l.take(s, min(s.listed, Shared<NT>::kList));
             l.sort(s, w, value_of(hi), value_of(lo), before);
             if (l.locate(s, by_mass, target)) return s.before;
             __syncthreads();
@@ -627,7 +638,7 @@ struct RowBins {
     __device__ __forceinline__ void add(float x, uint32_t *count, u64 *mass)
     {
         if (!(x > -INFINITY)) return;
-        const int b = (int)fminf((w.top - x) * bin_scale, (float)(BINS - 1));
+        const int b = value_bin(w.top, x, bin_scale, BINS);
         const double t = w.t(x);
         const u64 m = w.units_at(t);
         atomicAdd(&count[b], 1u);
