@@ -797,10 +797,13 @@ int residual_norm_rows(const residual_norm_desc *desc, int64_t m, int64_t n, voi
  * 0, kept 1.  NaN as top_p or min_p: off.  A row without a finite logit: id -1,
  * logprob -infinity, kept 0; a row with a NaN or +infinity: id -1, logprob NaN,
  * kept 0.
- * Weights and sums are those of 64-bit arithmetic: weights within 1.5e-14, summed
- * as whole multiples of 2^-52 of the largest weight, or of 2^-60 of the row's sum
- * where that is more (with top-k, or min-p alone: of 2^-60 of n_vocab), so that
- * results do not depend on the order of a sum: the same bits at every call.
+ * Weights and sums are those of 64-bit arithmetic: a weight 2^-d is off by
+ * 1.6e-14 + 3.1e-16 d of itself at most, and weights are summed as whole multiples
+ * of 2^-52 of the largest, or of 2^-60 of the row's sum where that is more (with
+ * top-k, or min-p alone: of 2^-60 of n_vocab), so that sums do not depend on their
+ * order.  The mass of a row of which nothing is cut may be a 64-bit floating-point
+ * sum of the weights instead (1.3e-14 off at most), in a fixed order.  The same
+ * bits at every call.
  *   logits   [m][row_stride], aligned to the element, row_stride >= n_vocab when
  *            m > 1 (rows need no padding)
  * m >= 0, n_vocab > 0 (Q8_E_SHAPE); n_vocab <= 2^24, m <= 2^23, strides <= 2^32

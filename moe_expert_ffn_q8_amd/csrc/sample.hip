@@ -10,7 +10,9 @@
 // Weights exp((x - M) / T) are formed in 64 bits and summed as whole numbers of
 // 2^-52 of the largest (coarser where a row's sum S would pass 2^62): sums are
 // exact, whatever their order, and a border of top-p or of the random number
-// falls between tokens as it does in 64 bits.
+// falls between tokens as it does in 64 bits.  The mass of a row that nothing cuts
+// is, where its list answers it, the 64-bit floating-point sum instead, whose
+// order is fixed (its parts have no common unit before the largest is known).
 //
 // The logits are read once.  A workgroup takes a short row, a wave a part of a long
 // one, sums its weights where a filter needs the sum, and lists the logits that
@@ -45,9 +47,9 @@ constexpr float kReach = 64.0f;   // a histogram by value covers weights down to
 constexpr int kPlaces = 128;      // listed logits of a part
 constexpr int kRank = 128;        // how many maxima reach a list's bound, of 256: at most
 
-// 2^t for t <= 0 (2^-1000 below -1000), off by 1.5e-14 at most: 2^r on [-1/2, 1/2]
+// 2^t for t <= 0 (2^-1000 below -1000), off by 1.55e-14 at most: 2^r on [-1/2, 1/2]
 // as a polynomial of degree 9 that is 1 at 0 (the coefficients by the exchange
-// algorithm).  The nearest whole number comes from a sum with 1.5 * 2^52, whose
+// algorithm; 1.513e-14, the rest its roundings).  The nearest whole number comes from a sum with 1.5 * 2^52, whose
 // low bits hold it: the conversions, rounding and scaling instructions of fp64
 // issue at a quarter of the rate of its sums and products.
 __device__ __forceinline__ double exp2_64(double t)
@@ -492,7 +494,8 @@ __device__ __forceinline__ bool from_list(const SampleArgs &a, int64_t row, cons
                     whole = false;
                 }
             }
-            if (whole && sum != Settings::kFull) return false;
+            // (the last token that has mass is that of the whole units)
+            if (whole && (sum != Settings::kFull || set.u >= 1.0f)) return false;
             target = draw_target(set.u, head.mass);
         }
         if (!l.locate(s, step > 0, target)) return false;
