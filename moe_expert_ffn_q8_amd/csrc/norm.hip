@@ -9,10 +9,12 @@
 // Two arithmetics.  Where any row is fp32 or codes come out, everything between the
 // roundings is in 64 bits: a code of the row rule turns at a border, and then
 // does not hang on the order of a sum.  Where all rows are 16-bit floats it is
-// in 32 bits, with sums over threads in 64: conversions to and from 64 bits
-// issue at a quarter of the rate of other instructions and would bound the kernel
-// (16384 x 4096 bfloat16 181 us).  There a mean is taken of differences from a
-// thread's first value, so that a row far from 0 loses nothing.
+// in 32 bits, with means and sums over threads in 64: conversions to and from 64
+// bits issue at a quarter of the rate of other instructions, and everything in 64
+// would bound the kernel (16384 x 4096 bfloat16 181 us; the squares alone 173).
+// There v - mean is (v - p) - q with p the mean in 32 bits and q its rest, two
+// roundings of about the result's size wherever the mean and the largest values
+// lie.
 //
 // HBM bounds it: a row lies in the registers of one wave or workgroup, 8 values a
 // piece, so every tensor is read and written once; where rows are many a
@@ -214,20 +216,16 @@ __global__ __launch_bounds__(ROW > 256 ? ROW : 256) void norm_kernel(const NormA
         R pivot = 0, middle = 0, rstd;
         auto centred = [&](float x) { return a.layer ? ((R)x - pivot) - middle : (R)x; };
         auto stats = [&](double *p0, double *p1) {
+            double mean = 0.0;
             if (a.layer) {
-                pivot = WIDE ? (R)0 : (R)v[0][0];
-                middle = 0;
-                R s = 0;
-                int mine = 0;
+                double s = 0.0;
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const int left = n - at(p);
-                    mine += max(0, min(kPiece, left));
+                for (int p = 0; p < P; ++p)
 #pragma unroll
-                    for (int j = 0; j < kPiece; ++j) s += j < left ? (R)v[p][j] - pivot : (R)0;
-                }
-                const double mean = row_sum<ROW>((double)s + (double)pivot * mine, p0) * inv_n;
-                middle = (R)(mean - (double)pivot);
+                    for (int j = 0; j < kPiece; ++j) s += (double)v[p][j];     // (0 beyond the row)
+                mean = row_sum<ROW>(s, p0) * inv_n;
+                pivot = (R)mean;
+                middle = (R)(mean - (double)pivot);                            // (0 where R is double)
             }
             R s = 0;
 #pragma unroll
