@@ -727,8 +727,8 @@ int q8_0_embed_rows(const void *w, int r8, const int32_t *tokens, float scale, v
  *   layer 0:      norm(x) = x / sqrt(mean(x^2) + eps)
  *   layer not 0:  norm(x) = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
  * rounded to fp32, then to y's type.  Computed in 64 bits where a row is fp32 or
- * y is codes, in 32 bits (with sums over threads in 64) where all rows are of
- * 16-bit types.
+ * y is codes, in 32 bits (with means and sums over threads in 64) where all rows
+ * are of 16-bit types: there gate * a has to fit fp32.
  *   x        float rows [m][x_row_stride], aligned to the element
  *   weight   fp32 [n];  bias  fp32 [n], or NULL
  *   y        y_type Q8_T_F32, Q8_T_F16, Q8_T_BF16: rows aligned to the element;

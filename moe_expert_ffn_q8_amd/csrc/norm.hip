@@ -14,14 +14,15 @@
 // would bound the kernel (16384 x 4096 bfloat16 181 us; the squares alone 173).
 // There v - mean is (v - p) - q with p the mean in 32 bits and q its rest, two
 // roundings of about the result's size wherever the mean and the largest values
-// lie.
+// lie; squares that 32 bits do not hold are summed again in 64, and a row whose
+// root or differences may leave 32 bits is normed in 64, or scaled.
 //
 // HBM bounds it: a row lies in the registers of one wave or workgroup, 8 values a
 // piece, so every tensor is read and written once; where rows are many a
 // workgroup takes several, keeps the weights and has the next row's loads on
-// their way (16384 x 4096 bfloat16, residual, mean and bias: 133 us, 4.0 TB/s, 81%
-// of a copy; 257 x 4096 with a norm after the block and gates, to codes: 10 us, a
-// chain of loads, four reductions and stores).
+// their way (16384 x 4096 bfloat16, residual, mean and bias: 133 to 137 us, 3.9 to 4.0
+// TB/s, 79 to 81% of a copy; 257 x 4096 with a norm after the block and gates, to codes:
+// 10 us, a chain of loads, three reductions and stores).
 #include <type_traits>
 
 #include "i8_device.h"
@@ -109,14 +110,6 @@ __device__ __forceinline__ double row_sum(double s, double *part)
 
 __device__ __forceinline__ int type_bytes(int type) { return type == Q8_T_F32 ? 4 : type == Q8_T_I8 ? 1 : 2; }
 
-// One over the square root of a mean square and eps.
-__device__ __forceinline__ double inverse_root(double s, double) { return 1.0 / sqrt(s); }
-__device__ __forceinline__ float inverse_root(double s, float)
-{
-    if (!(s > 1e-30 && s < 1e37)) return (float)(1.0 / sqrt(s));
-    return __builtin_amdgcn_rsqf((float)s);
-}
-
 // A piece as loaded, of 16-bit values (HALF) or of any type.
 template <bool HALF>
 struct Piece {
@@ -153,6 +146,10 @@ __global__ __launch_bounds__(ROW > 256 ? ROW : 256) void norm_kernel(const NormA
     typedef typename std::conditional<WIDE, double, float>::type R;
     constexpr bool FEW = P <= (HALF ? 4 : 2);   // a row's loads all at once
     constexpr bool AHEAD = FEW && HALF;         // and the next row's before its work
+    // Rows far from 1 in code of their own: for few pieces no product for the others
+    // (16384 x 4096 137 us, with one 142), for many registers count (4096 x 14336
+    // with a norm after the block 188 apart, 164 with the product)
+    constexpr bool APART = !WIDE && P <= 2;
     constexpr int kPer = ROW == 64 ? 4 : 1, K = FEW ? P : 1;
     __shared__ double part[2][4][ROW / 64];
     __shared__ uint32_t part_max[2][ROW / 64];
@@ -212,11 +209,25 @@ __global__ __launch_bounds__(ROW > 256 ? ROW : 256) void norm_kernel(const NormA
             const int64_t next = row + (int64_t)gridDim.x * kPer;
             if (next < a.m) load_row(next);
         }
-        // the row held as (v - pivot) - middle, and 1 / sqrt(mean square + eps)
-        R pivot = 0, middle = 0, rstd;
-        auto centred = [&](float x) { return a.layer ? ((R)x - pivot) - middle : (R)x; };
+        // the row held as (lift v - pivot) - middle, and 1 / (lift sqrt(mean square +
+        // eps)).  far: a row whose differences or root may leave 32 bits; it is normed in
+        // 64 bits (APART), or has a power of two as its lift, which is 1 else
+        R lift = 1, pivot = 0, middle = 0, rstd;
+        double mean = 0.0, root = 0.0;
+        bool far = false;
+        auto centred = [&](float x, R by) { return a.layer ? fma((R)x, by, -pivot) - middle : (R)x * by; };
+        auto normed = [&](float x, auto apart) -> R {
+            if constexpr (decltype(apart)::value) return (R)(((double)x - mean) * root);
+            return centred(x, WIDE || APART ? (R)1 : lift) * rstd;
+        };
+        auto each_kind = [&](auto f) {
+            if (APART && far)
+                f(std::integral_constant<bool, APART>());
+            else
+                f(std::false_type());
+        };
         auto stats = [&](double *p0, double *p1) {
-            double mean = 0.0;
+            lift = 1;
             if (a.layer) {
                 double s = 0.0;
 #pragma unroll
@@ -233,82 +244,105 @@ __global__ __launch_bounds__(ROW > 256 ? ROW : 256) void norm_kernel(const NormA
                 const int left = n - at(p);
 #pragma unroll
                 for (int j = 0; j < kPiece; ++j) {
-                    const R d = j < left ? centred(v[p][j]) : (R)0;
+                    const R d = j < left ? centred(v[p][j], (R)1) : (R)0;
                     s = fma(d, d, s);
                 }
             }
             double sum = (double)s;
-            if (!WIDE && !(s > 1e-30f && s < 3e38f)) {     // squares that 32 bits do not hold
+            if (!WIDE && begin < n && !(s > 1e-30f && s < 3e38f)) {    // squares, or differences, that 32 bits do not hold
                 sum = 0.0;
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
                     const int left = n - at(p);
 #pragma unroll
                     for (int j = 0; j < kPiece; ++j) {
-                        const double d = j < left ? (double)centred(v[p][j]) : 0.0;
+                        float x = v[p][j];
+                        asm("" : "+v"(x));                 // (not the values converted above: registers)
+                        const double d = j < left ? (double)x - mean : 0.0;
                         sum = fma(d, d, sum);
                     }
                 }
             }
-            rstd = inverse_root(row_sum<ROW>(sum, p1) * inv_n + (double)a.eps, (R)0);
+            const double square = row_sum<ROW>(sum, p1) * inv_n + (double)a.eps;
+            far = false;
+            if (!WIDE && square > 1e-30 && square < 1e37) {
+                rstd = __builtin_amdgcn_rsqf((float)square);
+                return;
+            }
+            root = 1.0 / sqrt(square);
+            far = !WIDE && wave_uniform(root > 1e36 || root < 1e-36);
+            if (far && !APART) {
+                lift = root > 1e36 ? (R)0x1p64 : (R)0x1p-64;
+                mean *= (double)lift;
+                root /= (double)lift;
+                pivot = (R)mean;
+                middle = (R)(mean - (double)pivot);
+            }
+            rstd = (R)root;
         };
 
         if (a.residual) {
             if (a.post) stats(part[odd][0], part[odd][1]);
             uint8_t *ro = (uint8_t *)a.residual_out + row * a.ro_stride * type_bytes(a.r_type);
+            auto update = [&](auto apart) {
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const int i = at(p), left = n - i, k = FEW ? p : 0;
-                if (left <= 0) continue;
-                float rv[kPiece], gv[kPiece], pb[kPiece];
-                if (!FEW) {
-                    __builtin_amdgcn_sched_barrier(0);     // (one piece at a time: registers)
-                    rs[0].load(r, a.r_type, i, left);
-                    if (gate_row) gs[0].load(g, a.gate_type, i, left);
-                    if (a.post) load8(a.post_weight, Q8_T_F32, i, left, pw[0]);
-                }
-                (AHEAD ? rn : rs)[k].get(a.r_type, rv);
-                if (gate_row) (AHEAD ? gn : gs)[k].get(a.gate_type, gv);
-                else if (a.gate) load8(a.gate, a.gate_type, i, left, gv);
-                if (a.post_bias) load8(a.post_bias, Q8_T_F32, i, left, pb);
-#pragma unroll
-                for (int j = 0; j < kPiece; ++j) {
-                    R y = (R)v[p][j];
-                    if (a.post) {
-                        y = centred(v[p][j]) * rstd * (R)pw[k][j];
-                        if (a.post_bias) y += (R)pb[j];
+                for (int p = 0; p < P; ++p) {
+                    const int i = at(p), left = n - i, k = FEW ? p : 0;
+                    if (left <= 0) continue;
+                    float rv[kPiece], gv[kPiece], pb[kPiece];
+                    if (!FEW || decltype(apart)::value) __builtin_amdgcn_sched_barrier(0);   // (one piece at a time: registers)
+                    if (!FEW) {
+                        rs[0].load(r, a.r_type, i, left);
+                        if (gate_row) gs[0].load(g, a.gate_type, i, left);
+                        if (a.post) load8(a.post_weight, Q8_T_F32, i, left, pw[0]);
                     }
-                    if (a.gate) y *= (R)gv[j];
-                    v[p][j] = as_stored((float)fma((R)a.residual_scale, (R)rv[j], y), a.r_type);
-                    if (j >= left) v[p][j] = 0.0f;
+                    (AHEAD ? rn : rs)[k].get(a.r_type, rv);
+                    if (gate_row) (AHEAD ? gn : gs)[k].get(a.gate_type, gv);
+                    else if (a.gate) load8(a.gate, a.gate_type, i, left, gv);
+                    if (a.post_bias) load8(a.post_bias, Q8_T_F32, i, left, pb);
+#pragma unroll
+                    for (int j = 0; j < kPiece; ++j) {
+                        R y = (R)v[p][j];
+                        if (a.post) {
+                            y = normed(v[p][j], apart) * (R)pw[k][j];
+                            if (a.post_bias) y += (R)pb[j];
+                        }
+                        if (a.gate) y *= (R)gv[j];
+                        v[p][j] = as_stored((float)fma((R)a.residual_scale, (R)rv[j], y), a.r_type);
+                        if (j >= left) v[p][j] = 0.0f;
+                    }
+                    store8(ro, a.r_type, i, left, v[p]);
                 }
-                store8(ro, a.r_type, i, left, v[p]);
-            }
+            };
+            each_kind(update);
         }
 
         stats(part[odd][2], part[odd][3]);
         const bool codes = a.y_type == Q8_T_I8;
         uint8_t *y = (uint8_t *)a.y + row * a.y_stride * type_bytes(a.y_type);
         uint32_t amax = 0;
+        auto finish = [&](auto apart) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int i = at(p), left = n - i, k = FEW ? p : 0;
-            if (left <= 0) continue;
-            float b[kPiece];
-            if (!FEW) {
-                __builtin_amdgcn_sched_barrier(0);
-                load8(a.weight, Q8_T_F32, i, left, w[0]);
-            }
-            if (a.bias) load8(a.bias, Q8_T_F32, i, left, b);
+            for (int p = 0; p < P; ++p) {
+                const int i = at(p), left = n - i, k = FEW ? p : 0;
+                if (left <= 0) continue;
+                float b[kPiece];
+                if (!FEW || decltype(apart)::value) __builtin_amdgcn_sched_barrier(0);
+                if (!FEW) {
+                    load8(a.weight, Q8_T_F32, i, left, w[0]);
+                }
+                if (a.bias) load8(a.bias, Q8_T_F32, i, left, b);
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) {
-                R o = centred(v[p][j]) * rstd * (R)w[k][j];
-                if (a.bias) o += (R)b[j];
-                v[p][j] = (float)o;
-                if (j < left) amax = max(amax, abs_bits(v[p][j]));
+                for (int j = 0; j < kPiece; ++j) {
+                    R o = normed(v[p][j], apart) * (R)w[k][j];
+                    if (a.bias) o += (R)b[j];
+                    v[p][j] = (float)o;
+                    if (j < left) amax = max(amax, abs_bits(v[p][j]));
+                }
+                if (!WIDE || !codes) store8(y, a.y_type, i, left, v[p]);
             }
-            if (!WIDE || !codes) store8(y, a.y_type, i, left, v[p]);
-        }
+        };
+        each_kind(finish);
         if (!WIDE || !codes) continue;
 #pragma unroll
         for (int d = 32; d; d >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d));

@@ -1,5 +1,6 @@
 """Norms of 16-bit rows computed in 32 bits where those are short: a value far
-above a row's spread, against the 64-bit reference."""
+above a row's spread, rows at the ends of bfloat16's range, against the 64-bit
+reference."""
 import numpy as np
 import pytest
 
@@ -60,3 +61,54 @@ def test_outlier_channels(q, t, n):
     for layer in (False, True):
         _check(q, x, t, 1e-5, layer, (n, layer), rng=rng)
     _check(q, x + 100.0, t, 1e-5, True, (n, "far"), bias=_vec(rng, n, 0.1, 0.0), rng=rng)
+
+
+N_RANGE = [1, 5, 100, 505, 900, 2040, 4096, 8200, 20000, 65536]
+
+
+@pytest.mark.parametrize("size", [2e-40, 1e-39, 4e-39, 3e-38, 1e36, 1e37, 3e37, 8e37])
+@pytest.mark.parametrize("layer", [False, True])
+def test_ends_of_bfloat16(q, size, layer):
+    """Subnormal rows without an eps, and rows whose differences, or the sums of
+    them, leave 32 bits."""
+    rng = synth.rng("normends", str(size), str(layer))
+    for n in N_RANGE[layer:]:
+        x = np.clip(rng.normal(size=(3, n)) * size, -3.38e38, 3.38e38)
+        x[:, 0] = size                                         # (no row of zeros)
+        _check(q, x, "bf16", 0.0, layer, (size, n), rng=rng)
+
+
+@pytest.mark.parametrize("n", N_RANGE[1:])
+def test_largest_bfloat16_values(q, n):
+    """Values at the end itself, of either sign: one among the others' negatives,
+    halves, all but one alike."""
+    rng = synth.rng("normlargest", str(n))
+    big = 3.3895314e38
+    x = np.full((4, n), -big)
+    x[0, n // 2] = big
+    x[1, : n // 2] = big
+    x[2, 1:] = big
+    x[3] = rng.uniform(-1, 1, n) * big
+    for layer in (False, True):
+        _check(q, x, "bf16", 0.0, layer, (n, layer), bias=_vec(rng, n, 0.1, 0.0), rng=rng)
+
+
+@pytest.mark.parametrize("size", [1e-39, 1e38])
+@pytest.mark.parametrize("n", [100, 900, 4096, 9000])
+def test_ends_in_the_norm_after_a_block(q, n, size):
+    """post_weight's norm of such rows, into an ordinary stream, gated."""
+    rng = synth.rng("normpostends", str(n), str(size))
+    for layer in (False, True):
+        x = np.clip(rng.normal(size=(3, n)) * size, -3.38e38, 3.38e38)
+        g = to_gpu(x.astype(np.float32)).bfloat16()
+        r = to_gpu(rng.normal(size=(3, n)).astype(np.float32)).bfloat16()
+        pw, w, gate = _vec(rng, n), _vec(rng, n), _vec(rng, n, 0.1, 0.5)
+        import torch
+        out = q.residual_norm_rows(g, r, to_gpu(w), post_weight=to_gpu(pw), gate=to_gpu(gate), eps=0.0, layer=layer,
+                                   dtype=torch.bfloat16)
+        a, b = _norm(g.double().cpu().numpy(), pw.astype(np.float64), None, 0.0, layer)
+        rv, gv = r.double().cpu().numpy(), gate.astype(np.float64)
+        ops_ref.assert_rounded(out.residual.double().cpu().numpy(), gv * a + rv,
+                               np.abs(gv) * b + (3 * U + ops_ref.REL64) * (np.abs(gv * a) + np.abs(rv)), "bf16", "residual")
+        value, bound = _norm(out.residual.double().cpu().numpy(), w.astype(np.float64), None, 0.0, layer)
+        ops_ref.assert_rounded(out.y.double().cpu().numpy(), value, bound, "bf16", "y")
