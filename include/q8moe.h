@@ -679,7 +679,8 @@ int i8_up_gate_swiglu(const void *x, int x_type, int64_t x_row_stride, const flo
  *             residual_row_stride >= n when m > 1; NULL: none.  It may be y
  *             itself with y's row stride (the stream is updated in place) and
  *             must not overlap y otherwise.
- * Everything else as i8_matmul; an act that is none of these: Q8_E_UNSUPPORTED. */
+ * Strides of residual and y at most 2^32 (Q8_E_UNSUPPORTED).  Everything else as
+ * i8_matmul; an act that is none of these: Q8_E_UNSUPPORTED. */
 typedef enum q8_act {
     Q8_ACT_NONE = 0,
     Q8_ACT_RELU = 1,       /* max(v, 0) */

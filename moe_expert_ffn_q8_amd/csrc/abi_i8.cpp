@@ -35,6 +35,9 @@ int check_rows(const void *p, int64_t &stride, int64_t rows, int64_t k, int64_t 
     return stride > q8::kI8MaxRowBytes / bytes ? Q8_E_UNSUPPORTED : Q8_OK;
 }
 
+// Strides of the rows of an epilogue, in elements: byte offsets of rows fit 64 bits.
+constexpr int64_t kMaxStride = (int64_t)1 << 32;
+
 struct Epilogue {
     int act;
     const void *residual;
@@ -69,7 +72,9 @@ int i8_product(const void *x, int x_type, int64_t x_row_stride, const float *x_s
             if (!aligned(epi->residual, type_bytes(y_type))) return Q8_E_ALIGN;
             a.r_stride = m == 1 ? n : epi->r_stride;
             if (a.r_stride < n) return Q8_E_SHAPE;
+            if (a.r_stride > kMaxStride) return Q8_E_UNSUPPORTED;
         }
+        if (y_row_stride > kMaxStride) return Q8_E_UNSUPPORTED;
         a.epilogue = true;
         a.act = epi->act;
         a.residual = epi->residual;
