@@ -1106,15 +1106,16 @@ _ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "si
 
 
 def i8_matmul_act(x, w, w_scale, x_scale=None, bias=None, act="none", residual=None, y=None,
-                  dtype=torch.float32, ws=None):
+                  dtype=None, ws=None):
     """y = act(i8_matmul(...)) + residual, with act one of "none", "relu",
     "relu2" (its square), "gelu", "gelu_tanh", "silu"; residual: rows of y's
-    type [m][n], may be y itself (in place); the rest as for i8_matmul."""
+    type [m][n], may be y itself (in place); y is made, if not given, with
+    `dtype`, or of the residual's type, or fp32; the rest as for i8_matmul."""
     code = _ACTIVATIONS.get(act)
     if code is None:
         raise ValueError(f"act: {act!r}, expected one of {list(_ACTIVATIONS)}")
-    if y is None and residual is not None:
-        dtype = residual.dtype
+    if dtype is None:
+        dtype = torch.float32 if residual is None else residual.dtype
     return _i8_product("i8_matmul_act", _lib.i8_matmul_act, x, w, w_scale, x_scale, bias, y, dtype, ws,
                        False, code, residual)
 
