@@ -794,7 +794,7 @@ __device__ __forceinline__ Stretch stretch(const Settings &set, Held<T, NT, VECS
     constexpr int V = kVec<T>;
     auto larger = [](float p, float q) { return __builtin_elementwise_maximum(p, q); };
     Stretch r = {-INFINITY, x.extra, 0, 0, 0.0};
-    float lowest = x.extra;
+    float lowest = INFINITY;      // of this thread's vectors
 #pragma unroll
     for (int v = 0; v < VECS; ++v) {
         float y[V];
@@ -811,9 +811,10 @@ __device__ __forceinline__ Stretch stretch(const Settings &set, Held<T, NT, VECS
         __builtin_amdgcn_sched_barrier(0);
     }
     const bool bad = !(r.own_top < INFINITY);
+    // (counted where a vector holds -infinity, banned or beyond the stretch)
     uint32_t finite = 0;
     if (lowest == -INFINITY) x.each([&](float v, int) { finite += v > -INFINITY; });
-    else finite = VECS * V + 1;
+    else finite = VECS * V + (x.extra > -INFINITY);
     r.top = r.own_top;
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
