@@ -947,9 +947,14 @@ enum {
     Q8V_I8_TILES_128 = 2,              /* tiles of 128 x 128 */
     Q8V_I8_TILES_256 = 3,              /* tiles of 256 x 256, all of them whole */
     Q8V_I8_TILES_256_SOME_HALVES = 4,  /* the last round of them as 256 x 128 */
-    Q8V_I8_TILES_256_HALVES = 5        /* all of them as 256 x 128 */
+    Q8V_I8_TILES_256_HALVES = 5,       /* all of them as 256 x 128 */
+    Q8V_I8_TILES_K_HALVES = 6          /* tiles of 128 x 64, halves of k side by side */
 };
 int q8v_i8_form(int64_t n, int64_t k, int64_t m, int gated);
+
+/* q8v_i8_act_form: the same of i8_matmul_act, with whatever activation and
+ * residual (the only one to run Q8V_I8_TILES_K_HALVES). */
+int q8v_i8_act_form(int64_t n, int64_t k, int64_t m);
 
 /* moe_route: the grouping of (t,u) slots by expert that the MoE kernels use:
  * counts[e] (int32 [n_expert]), offsets[e] (int32 [n_expert+1], exclusive

@@ -171,6 +171,7 @@ _SIGS = {
     "sample_rows": (_int, [_vp, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp,
                            _size, _vp]),
     "q8v_i8_form": (_int, [_i64, _i64, _i64, _int]),
+    "q8v_i8_act_form": (_int, [_i64, _i64, _i64]),
     "logprob_workspace_bytes": (_size, [_i64, _i64, _i64]),
     "logprob_rows": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
                             _vp, _size, _vp]),

@@ -157,7 +157,7 @@ int i8_matmul_act(const void *x, int x_type, int64_t x_row_stride, const float *
                       y_row_stride, n, k, m, false, ws, ws_bytes, stream, &e);
 }
 
-int q8v_i8_form(int64_t n, int64_t k, int64_t m, int gated)
+static int i8_form(int64_t n, int64_t k, int64_t m, bool gated, bool epilogue)
 {
     if (int rc = check_i8_k(k)) return rc;
     if (n <= 0 || m <= 0) return Q8_E_SHAPE;
@@ -165,10 +165,15 @@ int q8v_i8_form(int64_t n, int64_t k, int64_t m, int gated)
         return Q8_E_UNSUPPORTED;
     q8::I8Args a = {};
     a.n = n; a.k = k; a.m = m;
-    if (q8::i8_inline_ok(a, gated != 0)) return Q8V_I8_STREAM_INLINE;
-    if (q8::i8_stream_ok(a, gated != 0)) return Q8V_I8_STREAM;
-    return q8::i8_gemm_form(a, gated != 0);
+    a.epilogue = epilogue;
+    if (q8::i8_inline_ok(a, gated)) return Q8V_I8_STREAM_INLINE;
+    if (q8::i8_stream_ok(a, gated)) return Q8V_I8_STREAM;
+    return q8::i8_gemm_form(a, gated);
 }
+
+int q8v_i8_form(int64_t n, int64_t k, int64_t m, int gated) { return i8_form(n, k, m, gated != 0, false); }
+
+int q8v_i8_act_form(int64_t n, int64_t k, int64_t m) { return i8_form(n, k, m, false, true); }
 
 static int check_logprob_sizes(int64_t m, int64_t n_vocab, int64_t n_top)
 {

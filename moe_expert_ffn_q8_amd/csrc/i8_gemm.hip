@@ -535,6 +535,14 @@ Plan plan(const I8Args &a, bool gated)
     return {true, large};
 }
 
+// Whether a product with an epilogue goes to the narrow kernel (512 x 14336 x 4096 59 ->
+// 45 us, 512 x 4096 x 4096 23 -> 20, 700 x 2048 x 2000 19.4 -> 16.8; a short k gains nothing:
+// 300 x 256 x 4096 9.7 -> 10.7)
+bool halves_of_k(const I8Args &a, const Plan &p)
+{
+    return a.epilogue && !p.large && p.grid.tiles_n * p.grid.tiles_m <= 128 && a.k >= 1024;
+}
+
 template <int YT, bool GATED, bool STREAM, bool EPI>
 int launch_form(const I8Args &a, hipStream_t stream)
 {
@@ -542,9 +550,7 @@ int launch_form(const I8Args &a, hipStream_t stream)
     const int tiles = p.grid.tiles_n * p.grid.tiles_m;
     if (!tiles) return Q8_E_UNSUPPORTED;
     if constexpr (EPI)
-        // (512 x 14336 x 4096 59 -> 45 us, 512 x 4096 x 4096 23 -> 20, 700 x 2048 x 2000
-        // 19.4 -> 16.8; a short k gains nothing: 300 x 256 x 4096 9.7 -> 10.7)
-        if (!p.large && tiles <= 128 && a.k >= 1024) {
+        if (halves_of_k(a, p)) {
             const TileGrid g = {p.grid.tiles_n, (int)((a.m + 63) / 64), 0};
             hipLaunchKernelGGL((i8_narrow_kernel<YT, STREAM>), dim3((unsigned)(g.tiles_n * g.tiles_m)), dim3(256), 0,
                                stream, a, g);
@@ -583,6 +589,7 @@ int i8_gemm_form(const I8Args &a, bool gated)
 {
     const Plan p = plan(a, gated);
     const int tiles = p.grid.tiles_n * p.grid.tiles_m;
+    if (halves_of_k(a, p)) return Q8V_I8_TILES_K_HALVES;
     if (!p.large) return Q8V_I8_TILES_128;
     return p.grid.whole == tiles ? Q8V_I8_TILES_256 : p.grid.whole ? Q8V_I8_TILES_256_SOME_HALVES
                                                                    : Q8V_I8_TILES_256_HALVES;
