@@ -146,6 +146,23 @@ __device__ __forceinline__ float activate(int act, float v)
     return v;
 }
 
+// N values, one branch for all.
+template <int N>
+__device__ __forceinline__ void activate_run(int act, float (&v)[N])
+{
+    auto each = [&](int code) {
+#pragma unroll
+        for (int r = 0; r < N; ++r) v[r] = activate(code, v[r]);
+    };
+    switch (act) {
+    case Q8_ACT_RELU: each(Q8_ACT_RELU); break;
+    case Q8_ACT_RELU2: each(Q8_ACT_RELU2); break;
+    case Q8_ACT_GELU: each(Q8_ACT_GELU); break;
+    case Q8_ACT_GELU_TANH: each(Q8_ACT_GELU_TANH); break;
+    case Q8_ACT_SILU: each(Q8_ACT_SILU); break;
+    }
+}
+
 // A value rounded to nearest even to the output's type.  (It is pinned as fp32
 // first: a last product merged with the conversion, as v_fma_mixlo_f16 does,
 // would round once where another kernel rounds twice.)

@@ -10,7 +10,7 @@
 // 1.8 GHz; 512 x 4096 x 14336 30 to 32 us on part of the device.  With few steps
 // the start and end of each tile are most of the time: 333 x 768 x 50257 25 to 29
 // us, of which the outputs are 10.  A long k with few outputs leaves CUs idle (k
-// is not split): 512 x 14336 x 4096 54 to 68 us.
+// is not split but in the narrow kernel): 512 x 14336 x 4096 53 to 68 us.
 //
 // Work decomposition:
 //  * Workgroup = WN x WM waves, tile TN weight rows x TM tokens; a wave
@@ -385,12 +385,22 @@ __device__ __forceinline__ void i8_tile(const I8Args &a, int64_t n0, int64_t m0,
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int s = acc[i][j][4 * q + r];
-                        v[r] = activate(a.act, a.bias ? i8_rescale(s, s_x[j], g4[r], b4[r])
-                                                      : i8_rescale(s, s_x[j], g4[r]));
+                        v[r] = a.bias ? i8_rescale(s, s_x[j], g4[r], b4[r]) : i8_rescale(s, s_x[j], g4[r]);
                     }
                     *(float4 *)(turn + li * 128 + 16 * ((2 * q + h) ^ ((li >> 1) & 7))) =
                         make_float4(v[0], v[1], v[2], v[3]);
                 }
+                // (by a loop over what the lane has just written: the activations' code
+                // 16 times in each turn would keep these loops from being unrolled, and
+                // the sums, then indexed by variables, in memory)
+                if (a.act != Q8_ACT_NONE)
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        float4 *o = (float4 *)(turn + li * 128 + 16 * ((2 * q + h) ^ ((li >> 1) & 7)));
+                        float v[4] = {o->x, o->y, o->z, o->w};
+                        activate_run<4>(a.act, v);
+                        *o = make_float4(v[0], v[1], v[2], v[3]);
+                    }
                 wave_lds_sync();
 #pragma unroll
                 for (int e = 0; e < kTurns; ++e) {
@@ -535,9 +545,10 @@ Plan plan(const I8Args &a, bool gated)
     return {true, large};
 }
 
-// Whether a product with an epilogue goes to the narrow kernel (512 x 14336 x 4096 59 ->
-// 45 us, 512 x 4096 x 4096 23 -> 20, 700 x 2048 x 2000 19.4 -> 16.8; a short k gains nothing:
-// 300 x 256 x 4096 9.7 -> 10.7)
+// Whether a product with an epilogue goes to the narrow kernel.  512 x k x 4096 on
+// tiles of 128 x 128 and on halves of k, us: k = 14336 54.1 and 40.8, 4096 18.6 and 16.7,
+// 2048 11.7 and 10.1, 1536 9.8 and 9.0, 1024 8.6 and 8.5, 768 7.9 and 8.1; 300 x 256 x 4096
+// 6.3 and 6.7.
 bool halves_of_k(const I8Args &a, const Plan &p)
 {
     return a.epilogue && !p.large && p.grid.tiles_n * p.grid.tiles_m <= 128 && a.k >= 1024;
