@@ -811,7 +811,9 @@ int residual_norm_rows(const residual_norm_desc *desc, int64_t m, int64_t n, voi
  * (Q8_E_UNSUPPORTED).  Outputs must not overlap the inputs.
  * Workspace: sample_workspace_bytes(m, n_vocab) bytes (0 for sizes the call
  * refuses), 256-byte aligned; contents need not be initialised; not shared by
- * calls that may run concurrently.
+ * calls that may run concurrently.  For rows of more than 4096 logits it holds, for
+ * each row of up to 2048, 1056 bytes per 2048 logits (a list of the largest of
+ * them) and 41 KB (should the row be read again): 90 MB for 512 rows of 262144.
  */
 size_t sample_workspace_bytes(int64_t m, int64_t n_vocab);
 

@@ -22,7 +22,8 @@
 // workgroup takes several, keeps the weights and has the next row's loads on
 // their way (16384 x 4096 bfloat16, residual, mean and bias: 133 to 137 us, 3.9 to 4.0
 // TB/s, 79 to 81% of a copy; 257 x 4096 with a norm after the block and gates, to codes:
-// 10 us, a chain of loads, three reductions and stores).
+// 10.6 us, a chain of loads, three reductions and stores; 16384 x 4096 with residual to
+// codes 162 to 168 us, from fp32 to fp32 213 to 235).
 #include <type_traits>
 
 #include "i8_device.h"

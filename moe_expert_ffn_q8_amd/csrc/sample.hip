@@ -28,10 +28,12 @@
 // error; the few rows where it is not are read again.
 //
 // Bounds: vector instructions for many long rows (512 x 262144 bfloat16, top-p:
-// parts 72 us, of which the pipe is busy 82%, join 13; HBM's floor 38); else the
-// chain of launches, round trips and barriers: 1 x 32000 5.8 + 11.6 us, 8 x 262144
-// 6.4 + 13, 333 x 50257 with settings of their own 20 + 13, and 7 + 28 where a row
-// is read again.
+// parts 59 us, of which the pipe is busy 75%, join 12; HBM's floor 38); else the
+// chain of launches, round trips and barriers: 1 x 32000 5.9 + 11.5 us, 8 x 262144
+// 6.6 + 13, 333 x 50257 with settings of their own 20 + 13, and 7 + 26 where a row
+// is read again.  These times are those of likely tokens all over the vocabulary and
+// masks of -infinity: a part that holds most of them, or one whose mask is finite and
+// leaves it fewer tokens than its list asks for, sends the row to be read again.
 #include "i8_device.h"
 #include "order_device.h"
 #include "q8_ops.h"
@@ -1011,9 +1013,10 @@ struct Work {
 };
 
 // A part is a wave's, without barriers.  What is done once a part (statistics,
-// bound, list) is 400 instructions, against 10 a logit; twice the vectors would
-// halve that share but leave nine waves to a CU (512 x 262144: 90 us against 72;
-// parts by four waves of as many vectors 89 to 150).
+// bound, list) is 400 instructions, against 7 a logit; twice the vectors would
+// halve that share but leave nine waves to a CU (512 x 262144, with a pass that
+// counted the logits: 90 us against 72; parts by four waves of as many vectors 89 to
+// 150).
 constexpr int kPartThreads = 64, kPartVecs = 8;
 
 template <int T>
